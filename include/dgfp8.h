@@ -462,6 +462,166 @@ dg_status dg_set_dense_plan(int instance, int splits);
 int dg_get_mk_alignment_for_contiguous_layout(void);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Mixture of experts: routing, expert layout, dispatch, combination
+ *
+ * What stands between a router's logits and the grouped GEMMs above, and
+ * between their outputs and the tokens.  All calls read their sizes from the
+ * host and everything else on the device, so a whole layer can be captured in
+ * a graph.  Element types are named by dg_dtype; 16-bit rows move in 16-byte
+ * pieces (see each call's alignment).  Statistics and sums are fp32.
+ */
+typedef enum dg_dtype { DG_F32 = 0, DG_BF16 = 1, DG_F16 = 2 } dg_dtype;
+typedef enum dg_route_score { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 } dg_route_score;
+
+/*
+ * Routing: the topk experts of each token and their weights.
+ *   logits  device, dtype [tokens, experts], row stride ld; element-aligned (rows
+ *           at 16-byte boundaries load faster)
+ *   bias    device, fp32 [experts] or NULL: added to the scores for the choice,
+ *           never for the weights (balancing of the experts' load)
+ *   indices device, int32 [tokens, topk], row stride ldi
+ *   weights device, fp32 [tokens, topk], row stride ldw
+ * Scores s: softmax over the token's logits, or the sigmoid of each.  Experts are
+ * ranked by s + bias, or without a bias by the logit itself (the same order,
+ * without the merging of close scores by rounding).  groups > 1 splits the experts into
+ * equal consecutive groups, of which only the best topk_groups take part: by
+ * their largest key (group_top2 == 0), or by the sum of the two largest s + bias
+ * (group_top2 != 0; a single available expert counts alone).  Of equal keys, and
+ * of equal groups, the lower number comes first.  Slot j of a token is its j-th
+ * largest key:
+ *   w_j = scale * s_j,  or  scale * s_j / (sum of the chosen s)  if renormalize != 0
+ * (0 if that sum is 0: every chosen sigmoid underflowed).
+ *   Unavailable experts: a logit or a bias of -inf takes an expert out.  Where
+ * fewer than topk are left, the last slots get index -1 and weight 0 (a row
+ * masked whole gets only those).  A NaN logit or bias (and, under softmax, a
+ * logit of +inf) also takes its expert out, and makes the token's weights NaN.
+ * Limits: 1 <= experts <= 1024, 1 <= topk <= min(64, experts), 1 <= topk_groups <=
+ * groups <= 64, experts % groups == 0, tokens <= 2^23.
+ * Errors: null pointers, sizes or enumerators outside these, ld < experts, ldi or
+ * ldw < topk -> DG_ERROR_INVALID_VALUE; experts, topk, groups or tokens above
+ * their maximum, strides over 2^40, misaligned pointers -> DG_ERROR_NOT_SUPPORTED.
+ */
+dg_status dg_route_topk(const void* logits, int dtype, int64_t ld, const float* bias,
+                        int32_t* indices, int64_t ldi, float* weights, int64_t ldw,
+                        int64_t tokens, int experts, int topk, int groups, int topk_groups,
+                        int group_top2, int score, int renormalize, float scale, void* stream);
+
+/*
+ * Gradient of dg_route_topk's weights with respect to the logits, the choice
+ * held fixed: dlogits[t, e] = sum_j dweights[t, j] * d w[t, j] / d logits[t, e].
+ * Every element of dlogits is written.
+ *   indices   as dg_route_topk wrote them: the experts of a token are distinct;
+ *             an index outside [0, experts) marks an unused slot
+ *   dweights  device, fp32 [tokens, topk], row stride ldw
+ *   dlogits   device, dtype [tokens, experts], row stride ldd; must not overlap logits
+ * Limits and errors as dg_route_topk (ldd < experts -> DG_ERROR_INVALID_VALUE).
+ */
+dg_status dg_route_topk_grad(const void* logits, int dtype, int64_t ld, const int32_t* indices, int64_t ldi,
+                             const float* dweights, int64_t ldw, void* dlogits, int64_t ldd,
+                             int64_t tokens, int experts, int topk, int score, int renormalize,
+                             float scale, void* stream);
+
+/*
+ * Expert layout for dg_m_grouped_*_gemm_nt_contiguous: a row for each slot (t, j)
+ * whose index is in [0, experts).  Experts follow one another in order, each
+ * from a multiple of 128 rows; within an expert the rows are in order of token and slot,
+ * so the layout is a function of the indices alone.
+ *   indices   device, int32 [tokens, topk], row stride ldi; others than 0..experts-1
+ *             have no row (dropped assignments)
+ *   rows      rows of the layout, a multiple of 128.
+ *             dg_expert_layout_rows() rows hold every routing; where fewer are
+ *             given, slots beyond them are dropped
+ *   m_indices device, int32 [rows]: expert of the row, -1 where it holds no slot
+ *   row_slot  device, int32 [rows]: t * topk + j of the row's slot, or -1
+ *   slot_row  device, int32 [tokens, topk], dense: row of the slot, or -1
+ *   counts    device, int32 [experts]: slots of each expert
+ *   ws        device, 16-byte aligned, dg_expert_layout_workspace_size() bytes
+ *             (contents do not matter; NULL where that is 0)
+ * Limits: experts <= 1024, topk <= 64, tokens * topk <= 2^30, rows < 2^31.
+ * Errors: rows % 128 != 0 -> DG_ERROR_MISALIGNED_LAYOUT; null pointers, negative
+ * sizes, ldi < topk, ws too small -> DG_ERROR_INVALID_VALUE; beyond the limits, or
+ * misaligned -> DG_ERROR_NOT_SUPPORTED.  tokens == 0 clears the layout.
+ */
+dg_status dg_expert_layout_contiguous(const int32_t* indices, int64_t ldi, int64_t tokens, int topk, int experts,
+                                      int64_t rows, int32_t* m_indices, int32_t* row_slot, int32_t* slot_row,
+                                      int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows that hold every routing of these sizes in the contiguous layout (a
+ * multiple of 128); 0 for sizes outside the limits. */
+int64_t dg_expert_layout_rows(int64_t tokens, int topk, int experts);
+
+/* Workspace bytes of the two layout calls: 0 up to 4096 slots. */
+size_t dg_expert_layout_workspace_size(int64_t tokens, int topk, int experts);
+
+/*
+ * Expert layout for dg_m_grouped_*_gemm_nt_masked: the slots of expert e get the
+ * rows e * max_m, e * max_m + 1, ... in order of token and slot; those past max_m
+ * are dropped.  masked_m receives min(slots of e, max_m).  Other arguments,
+ * limits (experts * max_m < 2^31) and errors as the contiguous call's.
+ *   row_slot  device, int32 [experts * max_m]
+ */
+dg_status dg_expert_layout_masked(const int32_t* indices, int64_t ldi, int64_t tokens, int topk, int experts,
+                                  int64_t max_m, int32_t* masked_m, int32_t* row_slot, int32_t* slot_row,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dispatch: quantizes each token's row once, as dg_per_token_cast_fp8 (the same
+ * codes and scales, bit for bit), and writes it to the row of each of its slots.
+ * Rows no slot has are left untouched.
+ *   x         device, dtype (DG_F32 or DG_BF16) [tokens, k], row stride ldx, rows at
+ *             16-byte boundaries
+ *   slot_row  device, int32 [tokens, topk], row stride lds; values outside
+ *             [0, rows) are skipped.  No row may be named twice.
+ *   q         device, E4M3 [rows, k], row stride ldq (bytes), rows at 16-byte boundaries
+ *   sf        device, fp32 [rows, k/128]: element (r, kb) at sf[r * sf_sm + kb * sf_sk]
+ * Limits: k % 128 == 0, topk <= 64, tokens <= 2^23.  Errors as the casts'.
+ */
+dg_status dg_dispatch_cast_fp8(const void* x, int dtype, int64_t ldx, const int32_t* slot_row, int64_t lds,
+                               void* q, int64_t ldq, float* sf, int64_t sf_sm, int64_t sf_sk,
+                               int64_t tokens, int topk, int64_t rows, int64_t k, int ue8m0, void* stream);
+
+/* Dispatch with the int8 cast of dg_per_token_cast_int8: q int8 [rows, k], sf
+ * fp32 [rows] with stride sf_s.  k % 16 == 0. */
+dg_status dg_dispatch_cast_int8(const void* x, int dtype, int64_t ldx, const int32_t* slot_row, int64_t lds,
+                                void* q, int64_t ldq, float* sf, int64_t sf_s,
+                                int64_t tokens, int topk, int64_t rows, int64_t k, void* stream);
+
+/*
+ * Combination: out[t] = sum_j weights[t, j] * y[slot_row[t, j]] over the slots that
+ * have a row, summed in slot order in fp32 and rounded once to out's type.  A
+ * token without any row gets zeros; rows no slot names are not read.
+ *   y         device, bf16 [rows, h], row stride ldy: the grouped GEMM's output
+ *   slot_row  device, int32 [tokens, topk], row stride lds; values outside [0, rows)
+ *             are skipped
+ *   weights   device, fp32 [tokens, topk], row stride ldw, or NULL: all ones (the
+ *             gradient of dispatching tokens to rows)
+ *   out       device, out_dtype (DG_BF16 or DG_F32) [tokens, h], row stride ldo
+ * Limits: h % 8 == 0, topk <= 64, tokens <= 2^23; rows of y and out at 16-byte
+ * boundaries.
+ */
+dg_status dg_combine(const void* y, int64_t ldy, const int32_t* slot_row, int64_t lds,
+                     const float* weights, int64_t ldw, void* out, int out_dtype, int64_t ldo,
+                     int64_t tokens, int topk, int64_t rows, int64_t h, void* stream);
+
+/*
+ * Gradient of dg_combine:
+ *   dy[r] = weights[t, j] * dout[t] where slot (t, j) has row r, zero elsewhere (bf16);
+ *   dweights[t, j] = <dout[t], y[slot_row[t, j]]> in fp32, 0 without a row.
+ *   dout      device, bf16 [tokens, h], row stride ldo
+ *   row_slot  device, int32 [rows], as the layout call wrote it beside slot_row: it
+ *             says which rows of dy to clear
+ *   dy        device, bf16 [rows, h], row stride lddy, must not overlap y or dout
+ *   dweights  device, fp32 [tokens, topk], row stride lddw
+ * Other arguments and limits as dg_combine.
+ */
+dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t ldy,
+                          const int32_t* slot_row, int64_t lds, const int32_t* row_slot,
+                          const float* weights, int64_t ldw, void* dy, int64_t lddy,
+                          float* dweights, int64_t lddw,
+                          int64_t tokens, int topk, int64_t rows, int64_t h, void* stream);
+
+/*
  * Width of the persistent GEMM grid in compute units (default: all CUs of the
  * current device).  Results never depend on it.  num_cus <= 0 restores the
  * default.  (Analog of set_num_sms: page ssnai.com DeepGEMM analysis.)

@@ -34,7 +34,24 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int
 
+_f32 = ctypes.c_float
+_sz = ctypes.c_size_t
+
 _SIGNATURES = {
+    "dg_route_topk": ([_p, _i32, _i64, _p, _p, _i64, _p, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                       _f32, _p], _i32),
+    "dg_route_topk_grad": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i32, _i32, _i32, _f32, _p],
+                           _i32),
+    "dg_expert_layout_contiguous": ([_p, _i64, _i64, _i32, _i32, _i64, _p, _p, _p, _p, _p, _sz, _p], _i32),
+    "dg_expert_layout_masked": ([_p, _i64, _i64, _i32, _i32, _i64, _p, _p, _p, _p, _sz, _p], _i32),
+    "dg_expert_layout_rows": ([_i64, _i32, _i32], _i64),
+    "dg_expert_layout_workspace_size": ([_i64, _i32, _i32], _sz),
+    "dg_dispatch_cast_fp8": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _i64, _i64, _i32, _p],
+                             _i32),
+    "dg_dispatch_cast_int8": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i64, _i64, _p], _i32),
+    "dg_combine": ([_p, _i64, _p, _i64, _p, _i64, _p, _i32, _i64, _i64, _i32, _i64, _i64, _p], _i32),
+    "dg_combine_grad": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i64, _i64,
+                         _p], _i32),
     "dg_status_string": ([_i32], ctypes.c_char_p),
     "dg_fp8_gemm_nt": ([_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p, _i64,
                         _i64, _i64, _i64, _p], _i32),
@@ -426,3 +443,5 @@ def set_dense_plan(instance: int, splits: int = 1) -> None:
 set_num_sms = set_num_cus
 get_num_sms = get_num_cus
 
+from .moe import (ExpertLayout, combine, combine_grad, dispatch_cast_fp8, dispatch_cast_int8,  # noqa: E402
+                  expert_layout_contiguous, expert_layout_masked, expert_layout_rows, route_topk, route_topk_grad)

@@ -9,9 +9,8 @@
 #include <cstdint>
 #include <initializer_list>
 
+#include "api_util.h"
 #include "dgfp8_internal.h"
-
-#define DG_EXPORT extern "C" __attribute__((visibility("default")))
 
 namespace dgfp8 {
 namespace {
@@ -41,18 +40,6 @@ int hw_cus() {
 // Width of the persistent grid.
 int device_cus() { return g_num_cus_override > 0 ? g_num_cus_override : hw_cus(); }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Strides (elements) and sizes no real buffer comes near: 2^40.  Rejecting
-// larger ones keeps every product of two of them inside int64 (in this file
-// and in the kernels' 64-bit offset arithmetic).
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
-bool strides_ok(std::initializer_list<int64_t> v) {
-  for (int64_t x : v)
-    if (x > kMaxStride) return false;
-  return true;
-}
-
 // Checks shared by the three GEMM variants.
 dg_status check_common(const void* a, int64_t lda, const void* sfa, int64_t sfa_sm, int64_t sfa_sk,
                        const void* b, int64_t ldb, const void* sfb, int64_t sfb_sn, int64_t sfb_sk,
@@ -69,8 +56,6 @@ dg_status check_common(const void* a, int64_t lda, const void* sfa, int64_t sfa_
   if (!aligned(sfa, 4) || !aligned(sfb, 4)) return DG_ERROR_NOT_SUPPORTED;
   return DG_SUCCESS;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Static instance choice: estimated time = rounds of persistent tiles x tile
 // area x a per-instance cost factor (relative cycles per output element,

@@ -1,0 +1,144 @@
+// Combination of the experts' rows into tokens, and its gradient.
+//
+// Mathematics.  out[t] = sum_j w[t,j] y[row(t,j)] over the slots that have a row,
+// summed in slot order in fp32 and rounded once.  Gradient:
+//   dy[row(t,j)] = w[t,j] dout[t], zero on rows that hold no slot;
+//   dw[t,j] = <dout[t], y[row(t,j)]> in fp32, zero for slots without a row.
+// With unit weights the combination is also the gradient of the rows' dispatch.
+//
+// Bound by memory: every row is read once (and written once, in the gradient).
+// A thread owns eight columns of a token, and loads a batch of rows before it
+// adds the first, so that several 16-byte loads are in flight a lane.  The row
+// numbers and weights are the same for the whole workgroup.
+#include "elem_types.h"
+#include "moe_internal.h"
+
+namespace dgfp8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;    // rows in flight
+
+template <class OUT>
+__global__ void __launch_bounds__(kThreads) combine_kernel(CombineParams p) {
+  const int64_t t = blockIdx.x;
+  const int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
+  if (c >= p.h) return;
+  const uint16_t* y = (const uint16_t*)p.y + c;
+  const int32_t* rows = p.slot_row + t * p.lds;
+  const float* ws = p.weights ? p.weights + t * p.ldw : nullptr;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+    Eight<BF16> v[kBatch];
+    float w[kBatch];
+    bool there[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
+      there[b] = r >= 0 && r < p.rows;
+      w[b] = there[b] && ws ? ws[j0 + b] : 1.0f;
+      if (there[b]) v[b] = load_eight<BF16>(y + r * p.ldy);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (!there[b]) continue;   // what a dropped slot would weigh, or the row hold, does not matter
+      float x[8];
+      widen_eight(v[b], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[b], x[i], sum[i]);
+    }
+  }
+  store_eight<OUT>((typename OUT::store*)p.out + t * p.ldo + c, sum);
+}
+
+// Workgroups 0 .. tokens-1 take a token each; the rest clear the rows without a
+// slot, kClearRows apiece.
+constexpr int kClearRows = 64;
+
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(CombineGradParams p) {
+  if ((int64_t)blockIdx.x >= p.tokens) {
+    const int64_t r0 = ((int64_t)blockIdx.x - p.tokens) * kClearRows;
+    for (int64_t r = r0; r < r0 + kClearRows && r < p.rows; ++r) {
+      if (p.row_slot[r] >= 0) continue;
+      uint16_t* dst = (uint16_t*)p.dy + r * p.lddy;
+      for (int64_t c = threadIdx.x * 8; c < p.h; c += kThreads * 8) *(u32x4*)(dst + c) = (u32x4){0, 0, 0, 0};
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  const uint16_t* dout = (const uint16_t*)p.dout + t * p.ldo;
+  const uint16_t* y = (const uint16_t*)p.y;
+  uint16_t* dy = (uint16_t*)p.dy;
+  const int32_t* rows = p.slot_row + t * p.lds;
+  const float* ws = p.weights + t * p.ldw;
+  __shared__ float part[kThreads / 64][kBatch];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j0 = 0; j0 < p.topk; j0 += kBatch) {
+    float dot[kBatch], w[kBatch];
+    int64_t row[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      int64_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
+      if (r >= p.rows) r = -1;
+      row[b] = r;
+      w[b] = r >= 0 ? ws[j0 + b] : 0.0f;
+      dot[b] = 0.0f;
+    }
+    for (int64_t c = threadIdx.x * 8; c < p.h; c += kThreads * 8) {
+      const Eight<BF16> g = load_eight<BF16>(dout + c);
+      Eight<BF16> v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (row[b] >= 0) v[b] = load_eight<BF16>(y + row[b] * p.ldy + c);
+      float gx[8];
+      widen_eight(g, gx);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (row[b] < 0) continue;
+        float x[8], d[8];
+        widen_eight(v[b], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dot[b] = __builtin_fmaf(gx[i], x[i], dot[b]);
+          d[i] = w[b] * gx[i];
+        }
+        store_eight<BF16>(dy + row[b] * p.lddy + c, d);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) dot[b] += __shfl_xor(dot[b], off, 64);
+      if (lane == 0) part[wave][b] = dot[b];
+    }
+    __syncthreads();
+    const int j = j0 + (int)threadIdx.x;
+    if (threadIdx.x < kBatch && j < p.topk) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w2 = 0; w2 < kThreads / 64; ++w2) s += part[w2][threadIdx.x];
+      p.dweights[t * p.lddw + j] = s;   // 0 where the slot has no row
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+hipError_t launch_combine(const CombineParams& p, int out_dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)p.tokens, (unsigned)((p.h + kThreads * 8 - 1) / (kThreads * 8))), block(kThreads);
+  switch (out_dtype) {
+    case DG_F32: hipLaunchKernelGGL((combine_kernel<F32>), grid, block, 0, stream, p); break;
+    case DG_BF16: hipLaunchKernelGGL((combine_kernel<BF16>), grid, block, 0, stream, p); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_grad(const CombineGradParams& p, hipStream_t stream) {
+  const int64_t grid = p.tokens + (p.rows + kClearRows - 1) / kClearRows;
+  hipLaunchKernelGGL(combine_grad_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace dgfp8
