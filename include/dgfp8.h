@@ -461,6 +461,79 @@ dg_status dg_set_dense_plan(int instance, int splits);
  * (Page ssnai.com DeepGEMM analysis: the alignment query for contiguous MoE.) */
 int dg_get_mk_alignment_for_contiguous_layout(void);
 
+/* Element types of the calls below. */
+typedef enum dg_dtype { DG_F32 = 0, DG_BF16 = 1, DG_F16 = 2 } dg_dtype;
+
+/*
+ * ---------------------------------------------------------------------------
+ * int8 GEMM with a scale per token and per channel
+ *
+ *   D[m, n] = sfa[m] * sfb[n] * sum_k A[m, k] * B[n, k]
+ * A and B int8, K-major.  The sums are exact in int32; the result is
+ * fp32(sum) * sfa * sfb, each step rounded to fp32, then rounded once to D's type.  So it
+ * does not depend on tiles, splits or the grid width, and rows past a group's
+ * end, or padding, change nothing.  Scales: sfa[i * sfa_s] for row i, sfb[j * sfb_s]
+ * for channel j; any fp32 (a NaN or infinite scale shows in its row or column).
+ *   d     device, out_dtype (DG_BF16, DG_F16 or DG_F32), row stride ldd (elements);
+ *         16-byte stores where its rows lie on such boundaries, single elements
+ *         elsewhere, so any n and ldd >= n will do
+ * Alignment: K % 16 == 0 and K <= 131071; lda, ldb and the A/B base addresses are
+ * multiples of 16 bytes.  A K that is no multiple of 128 costs one more step a
+ * tile.  Violations return DG_ERROR_NOT_SUPPORTED.  The size contract above holds.
+ *
+ * The three forms take the tiles, plans, workspace and control calls of their
+ * FP8 counterparts (dg_set_dense_plan, dg_set_contiguous_plan, dg_set_num_cus).
+ */
+
+/* Dense.  ws as in dg_fp8_gemm_nt_ws (the workspaces are interchangeable); NULL:
+ * no K split. */
+dg_status dg_int8_gemm_nt(const void* a, int64_t lda, const float* sfa, int64_t sfa_s,
+                          const void* b, int64_t ldb, const float* sfb, int64_t sfb_s,
+                          void* d, int out_dtype, int64_t ldd,
+                          int64_t m, int64_t n, int64_t k,
+                          void* ws, size_t ws_bytes, void* stream);
+size_t dg_int8_gemm_nt_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* M-grouped, contiguous layout: groups, m_indices, ws and preconditions as in
+ * dg_m_grouped_fp8_gemm_nt_contiguous_ws.  b int8 [num_groups, n, k], sfb fp32
+ * [num_groups, n] with group stride sfb_group_stride. */
+dg_status dg_m_grouped_int8_gemm_nt_contiguous(const void* a, int64_t lda, const float* sfa, int64_t sfa_s,
+                                               const void* b, int64_t ldb, int64_t b_group_stride,
+                                               const float* sfb, int64_t sfb_s, int64_t sfb_group_stride,
+                                               void* d, int out_dtype, int64_t ldd,
+                                               const int32_t* m_indices, int64_t m_total,
+                                               int64_t n, int64_t k, int num_groups,
+                                               void* ws, size_t ws_bytes, void* stream);
+size_t dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(int64_t m_total, int64_t n, int64_t k,
+                                                           int num_groups);
+
+/* M-grouped, masked layout: masked_m and expected_m as in
+ * dg_m_grouped_fp8_gemm_nt_masked.  sfa fp32 [num_groups, max_m], sfb fp32
+ * [num_groups, n]. */
+dg_status dg_m_grouped_int8_gemm_nt_masked(const void* a, int64_t lda, int64_t a_group_stride,
+                                           const float* sfa, int64_t sfa_s, int64_t sfa_group_stride,
+                                           const void* b, int64_t ldb, int64_t b_group_stride,
+                                           const float* sfb, int64_t sfb_s, int64_t sfb_group_stride,
+                                           void* d, int out_dtype, int64_t ldd, int64_t d_group_stride,
+                                           const int32_t* masked_m, int num_groups,
+                                           int64_t max_m, int64_t n, int64_t k,
+                                           int64_t expected_m, void* stream);
+
+/*
+ * int8 cast of rows (a token's activations, or a channel's weights):
+ *   amax = max |x| over the row;  s = fl32(max(amax, 1e-4) / 127);
+ *   q = fl32(x / s) rounded to the nearest whole number, ties to even: -127..127.
+ * Bit-exact with this definition.  A row with an infinity or a NaN gets an
+ * infinite or NaN scale and unspecified codes: the product's row shows it.
+ *   x   device, dtype (DG_F32 or DG_BF16) [m, k], row stride ldx, rows at 16-byte
+ *       boundaries
+ *   q   device, int8 [m, k], row stride ldq, rows at 16-byte boundaries
+ *   sf  device, fp32 [m], stride sf_s
+ * Limits: k % 16 == 0, m <= 2^23.
+ */
+dg_status dg_per_token_cast_int8(const void* x, int dtype, int64_t ldx, void* q, int64_t ldq,
+                                 float* sf, int64_t sf_s, int64_t m, int64_t k, void* stream);
+
 /*
  * ---------------------------------------------------------------------------
  * Mixture of experts: routing, expert layout, dispatch, combination
@@ -471,7 +544,6 @@ int dg_get_mk_alignment_for_contiguous_layout(void);
  * a graph.  Element types are named by dg_dtype; 16-bit rows move in 16-byte
  * pieces (see each call's alignment).  Statistics and sums are fp32.
  */
-typedef enum dg_dtype { DG_F32 = 0, DG_BF16 = 1, DG_F16 = 2 } dg_dtype;
 typedef enum dg_route_score { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 } dg_route_score;
 
 /*

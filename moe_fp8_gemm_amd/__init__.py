@@ -49,6 +49,14 @@ _SIGNATURES = {
     "dg_dispatch_cast_fp8": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _i64, _i64, _i32, _p],
                              _i32),
     "dg_dispatch_cast_int8": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i64, _i64, _p], _i32),
+    "dg_int8_gemm_nt": ([_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i32, _i64, _i64, _i64, _i64, _p, _sz, _p], _i32),
+    "dg_int8_gemm_nt_workspace_size": ([_i64, _i64, _i64], _sz),
+    "dg_m_grouped_int8_gemm_nt_contiguous": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i32, _i64, _p,
+                                              _i64, _i64, _i64, _i32, _p, _sz, _p], _i32),
+    "dg_m_grouped_int8_gemm_nt_contiguous_workspace_size": ([_i64, _i64, _i64, _i32], _sz),
+    "dg_m_grouped_int8_gemm_nt_masked": ([_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i32,
+                                          _i64, _i64, _p, _i32, _i64, _i64, _i64, _i64, _p], _i32),
+    "dg_per_token_cast_int8": ([_p, _i32, _i64, _p, _i64, _p, _i64, _i64, _i64, _p], _i32),
     "dg_combine": ([_p, _i64, _p, _i64, _p, _i64, _p, _i32, _i64, _i64, _i32, _i64, _i64, _p], _i32),
     "dg_combine_grad": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i64, _i64,
                          _p], _i32),
@@ -443,5 +451,7 @@ def set_dense_plan(instance: int, splits: int = 1) -> None:
 set_num_sms = set_num_cus
 get_num_sms = get_num_cus
 
+from .int8 import (int8_gemm_nt, m_grouped_int8_gemm_nt_contiguous, m_grouped_int8_gemm_nt_masked,  # noqa: E402
+                   per_token_cast_int8)
 from .moe import (ExpertLayout, combine, combine_grad, dispatch_cast_fp8, dispatch_cast_int8,  # noqa: E402
                   expert_layout_contiguous, expert_layout_masked, expert_layout_rows, route_topk, route_topk_grad)

@@ -27,7 +27,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdgfp8.so")
-SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "cast_fp8.hip", "scratch.hip", "moe_route.hip",
+SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "gemm_int8.hip", "cast_fp8.hip", "scratch.hip", "moe_route.hip",
            "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip"]
 ARCH = "gfx950"
 
@@ -50,7 +50,7 @@ def _flags():
 # accumulators must live in VGPRs: force the VGPR-destination MFMA form (LLVM
 # otherwise picks the AGPR form for kernels allowed more than 256 VGPRs, and each
 # rescale then needs v_accvgpr_read/write moves).
-EXTRA_FLAGS = {"gemm_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("gemm_fp8.hip", "gemm_int8.hip")}
 
 
 RESOURCE_REPORT = os.path.join(BUILD_DIR, "resource_usage.txt")

@@ -277,7 +277,9 @@ dg_status launch(GemmInstance inst, Variant v, const GemmParams& p, int64_t tile
   int64_t grid = tile_bound < slots ? tile_bound : slots;
   if (grid <= 0) return DG_SUCCESS;
   if (tile_bound > INT_MAX) return DG_ERROR_NOT_SUPPORTED;
-  return launch_gemm(inst, v, p, (int)grid, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+  const hipError_t err = p.int8 ? launch_gemm_int8(inst, v, p, (int)grid, stream)
+                                : launch_gemm(inst, v, p, (int)grid, stream);
+  return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
 // The kernels address one group's operand rows with 32-bit byte offsets.
@@ -352,6 +354,24 @@ namespace {
 // same pointers, the format selects how a K block finds its scale.
 const float* sf_ptr(const void* p) { return static_cast<const float*>(p); }
 
+// Launch of a checked dense problem.
+dg_status run_dense(GemmParams p, void* ws, size_t ws_bytes, void* stream) {
+  // The plan (and so the summation order) follows the hardware CU count, never
+  // the grid-width override, so results do not depend on the override.  A
+  // split plan runs only when the caller's workspace holds it.
+  DensePlan plan = plan_dense(p.m, p.n, p.k, hw_cus(), ws != nullptr);
+  const int64_t need = plan_workspace_bytes(plan);
+  if (need > 0 && (int64_t)ws_bytes < need) plan = plan_dense(p.m, p.n, p.k, hw_cus(), false);
+  if (plan.splits > 1) {
+    p.counters = static_cast<int*>(ws);
+    p.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
+    p.splits = plan.splits;
+    p.kb_per_split = plan.kb_per_split;
+    return launch(plan.inst, kDenseSplitK, p, plan.tiles * plan.splits, static_cast<hipStream_t>(stream));
+  }
+  return launch(plan.inst, kDense, p, plan.tiles, static_cast<hipStream_t>(stream));
+}
+
 dg_status gemm_nt(const void* a, int64_t lda, const void* sfa, int64_t sfa_sm, int64_t sfa_sk, const void* b,
                   int64_t ldb, const void* sfb, int64_t sfb_sn, int64_t sfb_sk, void* d, int64_t ldd, int64_t m,
                   int64_t n, int64_t k, void* ws, size_t ws_bytes, void* stream, bool packed,
@@ -371,20 +391,7 @@ dg_status gemm_nt(const void* a, int64_t lda, const void* sfa, int64_t sfa_sm, i
   p.c = c; p.ldc = ldc;
   p.m = m; p.n = n; p.k = k; p.num_groups = 1;
   p.sf_packed = packed ? 1 : 0;
-  // The plan (and so the summation order) follows the hardware CU count, never
-  // the grid-width override, so results do not depend on the override.  A
-  // split plan runs only when the caller's workspace holds it.
-  DensePlan plan = plan_dense(m, n, k, hw_cus(), ws != nullptr);
-  const int64_t need = plan_workspace_bytes(plan);
-  if (need > 0 && (int64_t)ws_bytes < need) plan = plan_dense(m, n, k, hw_cus(), false);
-  if (plan.splits > 1) {
-    p.counters = static_cast<int*>(ws);
-    p.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
-    p.splits = plan.splits;
-    p.kb_per_split = plan.kb_per_split;
-    return launch(plan.inst, kDenseSplitK, p, plan.tiles * plan.splits, static_cast<hipStream_t>(stream));
-  }
-  return launch(plan.inst, kDense, p, plan.tiles, static_cast<hipStream_t>(stream));
+  return run_dense(p, ws, ws_bytes, stream);
 }
 
 }  // namespace
@@ -454,6 +461,63 @@ ContigDecision decide_contiguous(int64_t m_total, int64_t n, int64_t k, int num_
   return dec;
 }
 
+// Launches of a checked contiguous problem.
+dg_status run_contiguous(const GemmParams& p, void* ws, size_t ws_bytes, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t m_total = p.m, n = p.n, k = p.k;
+  const int num_groups = p.num_groups;
+  // Paired plan: when the groups average at least two 128-row blocks, pairs of
+  // consecutive blocks of one group run as 256-row tiles (the largest, most
+  // efficient tile) and the blocks left over as 128-row tiles in a second
+  // launch.  Both launches find their tiles on the device from m_indices, so
+  // the plan needs no host read and stays graph-capturable.  Each row's result
+  // is computed the same way whatever its tile, so no bit changes.
+  //
+  // With a workspace the second launch splits K over the CUs its few tiles
+  // leave idle (the split is chosen on the device from the listed blocks).
+  // The plan follows the hardware CU count, never the grid-width override, so
+  // the results (which the split's summation order affects) do not depend on
+  // the override.
+  const int64_t nblocks = m_total / kContiguousAlignment;
+  const ContigDecision dec = decide_contiguous(m_total, n, k, num_groups, ws != nullptr ? ws_bytes : 0);
+  if (dec.paired) {
+    const InstanceInfo hi = instance_info(kInstHuge);
+    GemmParams pp = p;
+    pp.contig_mode = 1;
+    dg_status st = launch(kInstHuge, kContiguous, pp, (nblocks / 2) * ceil_div(n, hi.bn), s);
+    if (st != DG_SUCCESS) return st;
+    GemmParams ps = p;
+    ps.contig_mode = 2;
+    const int64_t tiles_bound = std::min<int64_t>(num_groups, nblocks) * ceil_div(n, instance_info(dec.single).bn);
+    if (dec.split) {
+      const ContigSplit cs = contig_split(dec.single, nblocks, n, k, num_groups, hw_cus());
+      ps.counters = static_cast<int*>(ws);
+      ps.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
+      ps.splits = cs.cap;
+      ps.kb_per_split = (int)(k / 128);
+      ps.contig_split_units = cs.units;
+      return launch(dec.single, kContiguousSplitK, ps, std::max<int64_t>(tiles_bound, cs.units), s);
+    }
+    return launch(dec.single, kContiguous, ps, tiles_bound, s);
+  }
+  const ContigPlan pl = dec.plain;
+  const InstanceInfo hi = instance_info(pl.head);
+  GemmParams ph = p;
+  ph.m = pl.head_rows;
+  dg_status st = launch(pl.head, kContiguous, ph, (pl.head_rows / hi.bm) * ceil_div(n, hi.bn), s);
+  if (st != DG_SUCCESS || pl.head_rows == m_total) return st;
+  // The rest of the rows: the same problem seen from row head_rows on.
+  const int64_t r0 = pl.head_rows;
+  const InstanceInfo ti = instance_info(pl.tail);
+  GemmParams pt = p;
+  pt.a += r0 * p.lda;
+  pt.sfa += r0 * p.sfa_sm;
+  pt.d += r0 * p.ldd * (p.int8 && p.out_type == DG_F32 ? 2 : 1);   // in 16-bit units
+  pt.m_indices += r0;
+  pt.m = m_total - r0;
+  return launch(pl.tail, kContiguous, pt, (pt.m / ti.bm) * ceil_div(n, ti.bn), s);
+}
+
 dg_status grouped_contiguous(const void* a, int64_t lda, const void* sfa, int64_t sfa_sm, int64_t sfa_sk,
                              const void* b, int64_t ldb, int64_t b_group_stride, const void* sfb, int64_t sfb_sn,
                              int64_t sfb_sk, int64_t sfb_group_stride, void* d, int64_t ldd,
@@ -479,57 +543,7 @@ dg_status grouped_contiguous(const void* a, int64_t lda, const void* sfa, int64_
   p.m_indices = m_indices;
   p.m = m_total; p.n = n; p.k = k; p.num_groups = num_groups;
   p.sf_packed = packed ? 1 : 0;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  // Paired plan: when the groups average at least two 128-row blocks, pairs of
-  // consecutive blocks of one group run as 256-row tiles (the largest, most
-  // efficient tile) and the blocks left over as 128-row tiles in a second
-  // launch.  Both launches find their tiles on the device from m_indices, so
-  // the plan needs no host read and stays graph-capturable.  Each row's result
-  // is computed the same way whatever its tile, so no bit changes.
-  //
-  // With a workspace the second launch splits K over the CUs its few tiles
-  // leave idle (the split is chosen on the device from the listed blocks).
-  // The plan follows the hardware CU count, never the grid-width override, so
-  // the results (which the split's summation order affects) do not depend on
-  // the override.
-  const int64_t nblocks = m_total / kContiguousAlignment;
-  const ContigDecision dec = decide_contiguous(m_total, n, k, num_groups, ws != nullptr ? ws_bytes : 0);
-  if (dec.paired) {
-    const InstanceInfo hi = instance_info(kInstHuge);
-    GemmParams pp = p;
-    pp.contig_mode = 1;
-    st = launch(kInstHuge, kContiguous, pp, (nblocks / 2) * ceil_div(n, hi.bn), s);
-    if (st != DG_SUCCESS) return st;
-    GemmParams ps = p;
-    ps.contig_mode = 2;
-    const int64_t tiles_bound = std::min<int64_t>(num_groups, nblocks) * ceil_div(n, instance_info(dec.single).bn);
-    if (dec.split) {
-      const ContigSplit cs = contig_split(dec.single, nblocks, n, k, num_groups, hw_cus());
-      ps.counters = static_cast<int*>(ws);
-      ps.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
-      ps.splits = cs.cap;
-      ps.kb_per_split = (int)(k / 128);
-      ps.contig_split_units = cs.units;
-      return launch(dec.single, kContiguousSplitK, ps, std::max<int64_t>(tiles_bound, cs.units), s);
-    }
-    return launch(dec.single, kContiguous, ps, tiles_bound, s);
-  }
-  const ContigPlan pl = dec.plain;
-  const InstanceInfo hi = instance_info(pl.head);
-  GemmParams ph = p;
-  ph.m = pl.head_rows;
-  st = launch(pl.head, kContiguous, ph, (pl.head_rows / hi.bm) * ceil_div(n, hi.bn), s);
-  if (st != DG_SUCCESS || pl.head_rows == m_total) return st;
-  // The rest of the rows: the same problem seen from row head_rows on.
-  const int64_t r0 = pl.head_rows;
-  const InstanceInfo ti = instance_info(pl.tail);
-  GemmParams pt = p;
-  pt.a += r0 * lda;
-  pt.sfa += r0 * sfa_sm;
-  pt.d += r0 * ldd;
-  pt.m_indices += r0;
-  pt.m = m_total - r0;
-  return launch(pl.tail, kContiguous, pt, (pt.m / ti.bm) * ceil_div(n, ti.bn), s);
+  return run_contiguous(p, ws, ws_bytes, stream);
 }
 
 }  // namespace
@@ -589,6 +603,21 @@ DG_EXPORT dg_status dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_ws(
 
 namespace {
 
+// Launch of a checked masked problem.
+dg_status run_masked(const GemmParams& p, int64_t expected_m, void* stream) {
+  // Each group's B is streamed once per M tile: a 256-row tile covers groups
+  // of up to 256 rows in one pass.  When the caller expects few rows per group
+  // (decode: expected_m <= 64), 64-row tiles stage a quarter of the A rows and
+  // leave LDS for a third stage.  expected_m is a hint only: every instance
+  // computes each output element with the same operations in the same order,
+  // so the results are the same bits whichever instance runs.
+  const GemmInstance inst = (expected_m > 0 && expected_m <= 64) ? kInstDecode
+                            : (p.m > 128 ? kInstHuge : kInstLarge);
+  const InstanceInfo info = instance_info(inst);
+  const int64_t bound = (int64_t)p.num_groups * ceil_div(p.m, info.bm) * ceil_div(p.n, info.bn);
+  return launch(inst, kMasked, p, bound, static_cast<hipStream_t>(stream));
+}
+
 dg_status grouped_masked(const void* a, int64_t lda, int64_t a_group_stride, const void* sfa, int64_t sfa_sm,
                          int64_t sfa_sk, int64_t sfa_group_stride, const void* b, int64_t ldb, int64_t b_group_stride,
                          const void* sfb, int64_t sfb_sn, int64_t sfb_sk, int64_t sfb_group_stride, void* d,
@@ -617,17 +646,7 @@ dg_status grouped_masked(const void* a, int64_t lda, int64_t a_group_stride, con
   p.masked_m = masked_m;
   p.m = max_m; p.n = n; p.k = k; p.num_groups = num_groups;
   p.sf_packed = packed ? 1 : 0;
-  // Each group's B is streamed once per M tile: a 256-row tile covers groups
-  // of up to 256 rows in one pass.  When the caller expects few rows per group
-  // (decode: expected_m <= 64), 64-row tiles stage a quarter of the A rows and
-  // leave LDS for a third stage.  expected_m is a hint only: every instance
-  // computes each output element with the same operations in the same order,
-  // so the results are the same bits whichever instance runs.
-  const GemmInstance inst = (expected_m > 0 && expected_m <= 64) ? kInstDecode
-                            : (max_m > 128 ? kInstHuge : kInstLarge);
-  const InstanceInfo info = instance_info(inst);
-  const int64_t bound = (int64_t)num_groups * ceil_div(max_m, info.bm) * ceil_div(n, info.bn);
-  return launch(inst, kMasked, p, bound, static_cast<hipStream_t>(stream));
+  return run_masked(p, expected_m, stream);
 }
 
 }  // namespace
@@ -656,6 +675,118 @@ DG_EXPORT dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0(
   return grouped_masked(a, lda, a_group_stride, sfa, sfa_sm, sfa_sk, sfa_group_stride, b, ldb, b_group_stride, sfb,
                         sfb_sn, sfb_sk, sfb_group_stride, d, ldd, d_group_stride, masked_m, num_groups, max_m, n, k,
                         expected_m, stream, true);
+}
+
+// ---- int8 products: one scale per row of A and per row of B
+
+namespace {
+
+constexpr int64_t kMaxInt8K = 131071;   // the largest K whose sum of products of codes cannot leave int32
+
+dg_status check_int8(const void* a, int64_t lda, const float* sfa, int64_t sfa_s, const void* b, int64_t ldb,
+                     const float* sfb, int64_t sfb_s, const void* d, int64_t ldd, int out_dtype, int64_t n, int64_t k) {
+  if (out_dtype != DG_F32 && out_dtype != DG_BF16 && out_dtype != DG_F16) return DG_ERROR_INVALID_VALUE;
+  if (!a || !b || !d || !sfa || !sfb) return DG_ERROR_INVALID_VALUE;
+  if (sfa_s < 0 || sfb_s < 0) return DG_ERROR_INVALID_VALUE;
+  if (lda < k || ldb < k || ldd < n) return DG_ERROR_INVALID_VALUE;
+  if (!strides_ok({lda, ldb, ldd, sfa_s, sfb_s, n})) return DG_ERROR_NOT_SUPPORTED;
+  if (k == 0 || k % 16 != 0 || k > kMaxInt8K) return DG_ERROR_NOT_SUPPORTED;
+  if (lda % 16 != 0 || ldb % 16 != 0 || !aligned(a, 16) || !aligned(b, 16)) return DG_ERROR_NOT_SUPPORTED;
+  if (!aligned(d, out_dtype == DG_F32 ? 4 : 2) || !aligned(sfa, 4) || !aligned(sfb, 4)) return DG_ERROR_NOT_SUPPORTED;
+  return DG_SUCCESS;
+}
+
+GemmParams int8_params(const void* a, int64_t lda, const float* sfa, int64_t sfa_s, const void* b, int64_t ldb,
+                       const float* sfb, int64_t sfb_s, void* d, int64_t ldd, int64_t d_group_stride, int out_dtype,
+                       int64_t m, int64_t n, int64_t k, int num_groups) {
+  GemmParams p{};
+  p.int8 = 1;
+  p.a = static_cast<const uint8_t*>(a); p.lda = lda;
+  p.sfa = sfa; p.sfa_sm = sfa_s;
+  p.b = static_cast<const uint8_t*>(b); p.ldb = ldb;
+  p.sfb = sfb; p.sfb_sn = sfb_s;
+  p.d = static_cast<uint16_t*>(d); p.ldd = ldd; p.d_gs = d_group_stride;
+  p.m = m; p.n = n; p.k = k; p.num_groups = num_groups;
+  p.out_type = out_dtype;
+  const int64_t es = out_dtype == DG_F32 ? 4 : 2;
+  p.d_wide = aligned(d, 16) && (ldd * es) % 16 == 0 && (d_group_stride * es) % 16 == 0;
+  return p;
+}
+
+}  // namespace
+
+DG_EXPORT size_t dg_int8_gemm_nt_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || k % 16 != 0 || !dims_ok(m, n, k)) return 0;
+  return (size_t)plan_workspace_bytes(plan_dense(m, n, k, hw_cus(), true));
+}
+
+DG_EXPORT dg_status dg_int8_gemm_nt(const void* a, int64_t lda, const float* sfa, int64_t sfa_s, const void* b,
+                                    int64_t ldb, const float* sfb, int64_t sfb_s, void* d, int out_dtype, int64_t ldd,
+                                    int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes, void* stream) {
+  if (m < 0 || n < 0 || k < 0) return DG_ERROR_INVALID_VALUE;
+  if (m == 0 || n == 0) return DG_SUCCESS;
+  const dg_status st = check_int8(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, out_dtype, n, k);
+  if (st != DG_SUCCESS) return st;
+  if (!offsets_fit(m, lda, n, ldb)) return DG_ERROR_NOT_SUPPORTED;
+  if (ws && !aligned(ws, 16)) return DG_ERROR_NOT_SUPPORTED;
+  return run_dense(int8_params(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, 0, out_dtype, m, n, k, 1), ws, ws_bytes,
+                   stream);
+}
+
+DG_EXPORT size_t dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(int64_t m_total, int64_t n, int64_t k,
+                                                                     int num_groups) {
+  return dg_m_grouped_fp8_gemm_nt_contiguous_workspace_size(m_total, n, k / 128 * 128, num_groups);
+}
+
+DG_EXPORT dg_status dg_m_grouped_int8_gemm_nt_contiguous(
+    const void* a, int64_t lda, const float* sfa, int64_t sfa_s, const void* b, int64_t ldb, int64_t b_group_stride,
+    const float* sfb, int64_t sfb_s, int64_t sfb_group_stride, void* d, int out_dtype, int64_t ldd,
+    const int32_t* m_indices, int64_t m_total, int64_t n, int64_t k, int num_groups, void* ws, size_t ws_bytes,
+    void* stream) {
+  if (m_total < 0 || n < 0 || k < 0 || num_groups < 1) return DG_ERROR_INVALID_VALUE;
+  if (b_group_stride < 0 || sfb_group_stride < 0) return DG_ERROR_INVALID_VALUE;
+  if (m_total % kContiguousAlignment != 0) return DG_ERROR_MISALIGNED_LAYOUT;
+  if (m_total == 0 || n == 0) return DG_SUCCESS;
+  if (!m_indices) return DG_ERROR_INVALID_VALUE;
+  const dg_status st = check_int8(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, out_dtype, n, k);
+  if (st != DG_SUCCESS) return st;
+  if (b_group_stride % 16 != 0 || !aligned(m_indices, 4)) return DG_ERROR_NOT_SUPPORTED;
+  if (!strides_ok({b_group_stride, sfb_group_stride, m_total})) return DG_ERROR_NOT_SUPPORTED;
+  if (!offsets_fit(m_total, lda, n, ldb)) return DG_ERROR_NOT_SUPPORTED;
+  if (ws && !aligned(ws, 16)) return DG_ERROR_NOT_SUPPORTED;
+  GemmParams p = int8_params(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, 0, out_dtype, m_total, n, k, num_groups);
+  p.b_gs = b_group_stride;
+  p.sfb_gs = sfb_group_stride;
+  p.m_indices = m_indices;
+  return run_contiguous(p, ws, ws_bytes, stream);
+}
+
+DG_EXPORT dg_status dg_m_grouped_int8_gemm_nt_masked(
+    const void* a, int64_t lda, int64_t a_group_stride, const float* sfa, int64_t sfa_s, int64_t sfa_group_stride,
+    const void* b, int64_t ldb, int64_t b_group_stride, const float* sfb, int64_t sfb_s, int64_t sfb_group_stride,
+    void* d, int out_dtype, int64_t ldd, int64_t d_group_stride, const int32_t* masked_m, int num_groups,
+    int64_t max_m, int64_t n, int64_t k, int64_t expected_m, void* stream) {
+  if (max_m < 0 || n < 0 || k < 0 || num_groups < 1) return DG_ERROR_INVALID_VALUE;
+  if (a_group_stride < 0 || sfa_group_stride < 0 || b_group_stride < 0 || sfb_group_stride < 0 ||
+      d_group_stride < 0)
+    return DG_ERROR_INVALID_VALUE;
+  if (num_groups > kMaxMaskedGroups) return DG_ERROR_NOT_SUPPORTED;
+  if (max_m == 0 || n == 0) return DG_SUCCESS;
+  if (!masked_m) return DG_ERROR_INVALID_VALUE;
+  const dg_status st = check_int8(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, out_dtype, n, k);
+  if (st != DG_SUCCESS) return st;
+  if (a_group_stride % 16 != 0 || b_group_stride % 16 != 0 || !aligned(masked_m, 4)) return DG_ERROR_NOT_SUPPORTED;
+  if (!strides_ok({a_group_stride, sfa_group_stride, b_group_stride, sfb_group_stride, d_group_stride, max_m}))
+    return DG_ERROR_NOT_SUPPORTED;
+  if (!offsets_fit(max_m, lda, n, ldb)) return DG_ERROR_NOT_SUPPORTED;
+  GemmParams p = int8_params(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, d_group_stride, out_dtype, max_m, n, k,
+                             num_groups);
+  p.a_gs = a_group_stride;
+  p.sfa_gs = sfa_group_stride;
+  p.b_gs = b_group_stride;
+  p.sfb_gs = sfb_group_stride;
+  p.masked_m = masked_m;
+  return run_masked(p, expected_m, stream);
 }
 
 namespace {

@@ -218,3 +218,16 @@ DG_EXPORT dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y
                       tokens, rows, h, topk};
   return of(launch_combine_grad(p, static_cast<hipStream_t>(stream)));
 }
+
+DG_EXPORT dg_status dg_per_token_cast_int8(const void* x, int dtype, int64_t ldx, void* q, int64_t ldq, float* sf,
+                                           int64_t sf_s, int64_t m, int64_t k, void* stream) {
+  if (dtype != DG_F32 && dtype != DG_BF16) return DG_ERROR_INVALID_VALUE;
+  if (m < 0 || k < 0 || sf_s < 0) return DG_ERROR_INVALID_VALUE;
+  if (m == 0 || k == 0) return DG_SUCCESS;
+  dg_status st = check_rows(x, ldx, k, elem_bytes(dtype));
+  if (st != DG_SUCCESS || (st = check_rows(q, ldq, k, 1)) != DG_SUCCESS) return st;
+  if (!sf) return DG_ERROR_INVALID_VALUE;
+  if (k % 16 != 0 || m > kMaxTokens || !aligned(sf, 4) || !strides_ok({sf_s})) return DG_ERROR_NOT_SUPPORTED;
+  DispatchParams p{x, ldx, nullptr, 0, 1, m, m, k, static_cast<uint8_t*>(q), ldq, sf, sf_s, 0, 0};
+  return of(launch_cast_int8(p, dtype, static_cast<hipStream_t>(stream)));
+}

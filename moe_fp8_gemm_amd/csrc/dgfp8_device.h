@@ -21,6 +21,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kKBlock = 128;      // width of a scale block along K == K of one MFMA
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // s_waitcnt immediate (gfx9 encoding): vmcnt <= VM, lgkmcnt == 0, expcnt unconstrained.
@@ -52,12 +53,18 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return (const uint8_t*)(uintptr_t)(((uint64_t)hi << 32) | lo);
 }
+// Wait states the compiler does not insert before inline asm (a test scans the
+// built code for both):
+//  * M0 written by a scalar instruction, then read by a load to LDS: 1, hence the s_nop;
+//  * a scalar register written by a vector instruction (v_readfirstlane), then
+//    read by the load: 5.  The base has to live in scalar registers, as it does
+//    where the compiler knows it to be the same in all lanes.
 __device__ __forceinline__ void dma16(const uint8_t* sbase, uint32_t voff, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1"
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(uniform_ptr(sbase)), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 __device__ __forceinline__ void dma4(const float* vaddr, uint32_t lds) {
-  asm volatile("global_load_lds_dword %0, off"
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off"
                :: "v"(vaddr), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 
@@ -73,6 +80,12 @@ __device__ __forceinline__ void lds_barrier() {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const f32x2 v = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Two fp32 -> packed fp16 pair, round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const f16x2 v = {(_Float16)lo, (_Float16)hi};
+  return __builtin_bit_cast(uint32_t, v);
 }
 
 // Two 16-byte LDS reads of a fragment (offsets of this lane's two slots).

@@ -53,6 +53,9 @@ struct GemmParams {
   // (and at most the K blocks); the workspace holds contig_split_units partial
   // tiles.  A host constant, so the split never depends on the grid width.
   int contig_split_units;
+  // int8 (launch_gemm_int8): D's type (dg_dtype); d_wide: 16-byte stores fit D's
+  // rows.  sfa / sfb are then [rows] at stride sfa_sm and [n] at stride sfb_sn.
+  int int8, out_type, d_wide;
 };
 
 // Largest number of 128-row blocks (m_total / 128) a paired contiguous plan takes.
@@ -78,6 +81,9 @@ InstanceInfo instance_info(GemmInstance inst);
 
 hipError_t launch_gemm(GemmInstance inst, Variant v, const GemmParams& p, int grid,
                        hipStream_t stream);
+
+// The int8 instances (p.int8): the same tiles and variants.
+hipError_t launch_gemm_int8(GemmInstance inst, Variant v, const GemmParams& p, int grid, hipStream_t stream);
 
 struct CastParams {
   const void* x;

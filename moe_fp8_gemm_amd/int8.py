@@ -1,0 +1,115 @@
+"""int8 GEMMs with a scale per token and per channel, and the int8 cast.
+
+Operands are pairs ``(codes, scales)`` as in the FP8 GEMMs: int8 codes, K-major,
+and fp32 scales, one for each row of A and of B (any stride).  Outputs are
+bfloat16, float16 or float32 of any width and row stride.  Argument marshalling
+only; the contract is in ``include/dgfp8.h``.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _AUTO, _check, _stream, _workspace_arg, lib
+from .moe import _DTYPES, _device, _ld, _out, _same_device
+
+Pair = Tuple[torch.Tensor, torch.Tensor]
+
+
+def _operand(pair: Pair, name: str, dim: int) -> Pair:
+    q, s = pair
+    _device(q, name, (torch.int8,), dim)
+    if s.dtype != torch.float32 or not s.is_cuda:
+        raise TypeError(f"sf{name} must be a float32 device tensor")
+    if s.shape != q.shape[:-1]:
+        raise ValueError(f"sf{name} must have shape {tuple(q.shape[:-1])}, got {tuple(s.shape)}")
+    return q, s
+
+
+def _result(d: torch.Tensor, shape) -> torch.Tensor:
+    _device(d, "d", tuple(_DTYPES), len(shape))
+    if tuple(d.shape) != tuple(shape):
+        raise ValueError(f"d must have shape {tuple(shape)}, got {tuple(d.shape)}")
+    return d
+
+
+def _rows(t: torch.Tensor) -> int:
+    """Row stride of a [groups, rows, columns] tensor."""
+    return t.stride(1) if t.shape[1] > 1 else max(t.stride(1), t.shape[2])
+
+
+def per_token_cast_int8(x: torch.Tensor, q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None) -> Pair:
+    """x bf16 or fp32 [m, k] -> (int8 codes [m, k], fp32 scales [m]): s = max(amax, 1e-4) / 127, q = round(x / s)."""
+    _device(x, "x", (torch.bfloat16, torch.float32), 2)
+    m, k = x.shape
+    q = _out(q, (m, k), torch.int8, x, "q")
+    if sf is None:
+        sf = torch.empty(m, dtype=torch.float32, device=x.device)
+    if sf.dtype != torch.float32 or not sf.is_cuda or tuple(sf.shape) != (m,):
+        raise ValueError(f"sf must be an fp32 device tensor of shape {(m,)}")
+    _same_device(x, q=q, sf=sf)
+    _check(lib.dg_per_token_cast_int8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), q.data_ptr(), _ld(q), sf.data_ptr(),
+                                      sf.stride(0), m, k, _stream()), "dg_per_token_cast_int8")
+    return q, sf
+
+
+def int8_gemm_nt(a: Pair, b: Pair, d: torch.Tensor, workspace=_AUTO) -> torch.Tensor:
+    """d[m, n] = sfa[m] * sfb[n] * sum_k a[m, k] * b[n, k], the sums exact.
+
+    a = (codes [m, k], sfa [m]); b = (codes [n, k], sfb [n]); d bf16, fp16 or fp32 [m, n] is overwritten and returned.
+    ``workspace`` as for ``fp8_gemm_nt``; it changes the time only, never a bit.
+    """
+    (qa, sa), (qb, sb) = _operand(a, "a", 2), _operand(b, "b", 2)
+    (m, k), n = qa.shape, qb.shape[0]
+    if qb.shape[1] != k:
+        raise ValueError(f"a has {k} columns, b has {qb.shape[1]}")
+    _result(d, (m, n))
+    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d)
+    ws_ptr, ws_bytes = _workspace_arg(workspace, d.device, int(lib.dg_int8_gemm_nt_workspace_size(m, n, k)))
+    _check(lib.dg_int8_gemm_nt(qa.data_ptr(), _ld(qa), sa.data_ptr(), sa.stride(0), qb.data_ptr(), _ld(qb),
+                               sb.data_ptr(), sb.stride(0), d.data_ptr(), _DTYPES[d.dtype], _ld(d), m, n, k,
+                               ws_ptr or None, ws_bytes, _stream()), "dg_int8_gemm_nt")
+    return d
+
+
+def m_grouped_int8_gemm_nt_contiguous(a: Pair, b: Pair, d: torch.Tensor, m_indices: torch.Tensor,
+                                      workspace=_AUTO) -> torch.Tensor:
+    """Contiguous layout: a = (codes [m_total, k], sfa [m_total]), b = (codes [G, n, k], sfb [G, n]), d [m_total, n],
+    m_indices int32 [m_total]; rows of -1 are left untouched (see ``m_grouped_fp8_gemm_nt_contiguous``)."""
+    (qa, sa), (qb, sb) = _operand(a, "a", 2), _operand(b, "b", 3)
+    (m, k), (g, n, _) = qa.shape, qb.shape
+    if qb.shape[2] != k:
+        raise ValueError(f"a has {k} columns, b has {qb.shape[2]}")
+    _result(d, (m, n))
+    _device(m_indices, "m_indices", (torch.int32,), 1)
+    if m_indices.shape[0] != m:
+        raise ValueError(f"m_indices must have {m} elements, got {m_indices.shape[0]}")
+    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d, m_indices=m_indices)
+    need = int(lib.dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(m, n, k, g))
+    ws_ptr, ws_bytes = _workspace_arg(workspace, d.device, need)
+    _check(lib.dg_m_grouped_int8_gemm_nt_contiguous(
+        qa.data_ptr(), _ld(qa), sa.data_ptr(), sa.stride(0), qb.data_ptr(), _rows(qb), qb.stride(0), sb.data_ptr(),
+        sb.stride(1), sb.stride(0), d.data_ptr(), _DTYPES[d.dtype], _ld(d), m_indices.data_ptr(), m, n, k, g,
+        ws_ptr or None, ws_bytes, _stream()), "dg_m_grouped_int8_gemm_nt_contiguous")
+    return d
+
+
+def m_grouped_int8_gemm_nt_masked(a: Pair, b: Pair, d: torch.Tensor, masked_m: torch.Tensor,
+                                  expected_m: int) -> torch.Tensor:
+    """Masked layout: a = (codes [G, max_m, k], sfa [G, max_m]), b = (codes [G, n, k], sfb [G, n]), d [G, max_m, n],
+    masked_m int32 [G] read on the device; rows >= masked_m[g] are left untouched.  ``expected_m``: a hint."""
+    (qa, sa), (qb, sb) = _operand(a, "a", 3), _operand(b, "b", 3)
+    (g, m, k), n = qa.shape, qb.shape[1]
+    if qb.shape[0] != g or qb.shape[2] != k:
+        raise ValueError(f"b must have shape {(g, n, k)}, got {tuple(qb.shape)}")
+    _result(d, (g, m, n))
+    _device(masked_m, "masked_m", (torch.int32,), 1)
+    if masked_m.shape[0] != g:
+        raise ValueError(f"masked_m must have {g} elements, got {masked_m.shape[0]}")
+    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d, masked_m=masked_m)
+    _check(lib.dg_m_grouped_int8_gemm_nt_masked(
+        qa.data_ptr(), _rows(qa), qa.stride(0), sa.data_ptr(), sa.stride(1), sa.stride(0), qb.data_ptr(), _rows(qb),
+        qb.stride(0), sb.data_ptr(), sb.stride(1), sb.stride(0), d.data_ptr(), _DTYPES[d.dtype], _rows(d), d.stride(0),
+        masked_m.data_ptr(), g, m, n, k, int(expected_m), _stream()), "dg_m_grouped_int8_gemm_nt_masked")
+    return d

@@ -14,6 +14,8 @@ Modules:
 * ``gemm``  -- dense, M-grouped contiguous and M-grouped masked references:
   decode exactly, scale per K block, accumulate in float64, round once.
 * ``exact`` -- the same GEMM in exact rational arithmetic, for tiny shapes.
+* ``int8``  -- int8 cast per row, and the product with scales per row of either operand.
+* ``moe``   -- routing and its gradient, expert layouts, combination and its gradient.
 * ``ue8m0`` -- packing of exponent-only scales, four per int32 word.
 
 Every function is pinned by CPU tests against closed forms, library decoders,
@@ -24,4 +26,4 @@ the quotient, a skipped fp32 rounding, ties away from zero, UE8M0 rounded down,
 no amax floor, bf16 truncation or double rounding, K-block scale order, the B
 scale index, a spurious factor, a dropped K block) and checks that a pin fails.
 """
-from . import bf16, e4m3, exact, gemm, quant, ue8m0  # noqa: F401
+from . import bf16, e4m3, exact, gemm, int8, moe, quant, ue8m0  # noqa: F401

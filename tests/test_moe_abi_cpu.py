@@ -1,4 +1,4 @@
-"""Refusals of the mixture-of-experts entry points: every bad argument comes back
+"""Refusals of the mixture-of-experts and int8 entry points: every bad argument comes back
 as a status before anything is launched, and the binding rejects wrong tensors.
 Addresses are fake and never dereferenced."""
 import ctypes
@@ -137,13 +137,65 @@ def test_combine_grad(kw, status):
     assert call(lib.dg_combine_grad, COMBINE_GRAD, **kw) == status
 
 
+CAST8 = dict(x=P, dtype=1, ldx=256, q=P, ldq=256, sf=P, sf_s=1, m=4, k=256, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(m=0), OK), (dict(k=0), OK), (dict(x=None), INVALID), (dict(q=None), INVALID), (dict(sf=None), INVALID),
+    (dict(m=-1), INVALID), (dict(dtype=2), INVALID), (dict(ldx=255), INVALID), (dict(k=8, ldx=8), UNSUPPORTED),
+    (dict(q=P + 8), UNSUPPORTED), (dict(m=(1 << 23) + 1), UNSUPPORTED)])
+def test_cast_int8(kw, status):
+    assert call(lib.dg_per_token_cast_int8, CAST8, **kw) == status
+
+
+GEMM8 = dict(a=P, lda=256, sfa=P, sfa_s=1, b=P, ldb=256, sfb=P, sfb_s=1, d=P, out=1, ldd=64, m=32, n=64, k=256, ws=None,
+             ws_bytes=0, stream=None)
+GEMM8_CASES = [
+    (dict(n=0), OK), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(d=None), INVALID), (dict(sfa=None), INVALID),
+    (dict(sfb=None), INVALID), (dict(out=3), INVALID), (dict(lda=255), INVALID), (dict(ldb=128), INVALID),
+    (dict(ldd=63), INVALID), (dict(sfa_s=-1), INVALID), (dict(k=-1), INVALID), (dict(k=0), UNSUPPORTED),
+    (dict(k=200), UNSUPPORTED), (dict(k=131072, lda=131072, ldb=131072), UNSUPPORTED), (dict(lda=264), UNSUPPORTED),
+    (dict(a=P + 8), UNSUPPORTED), (dict(b=P + 4), UNSUPPORTED), (dict(d=P + 1), UNSUPPORTED), (dict(sfa=P + 2), UNSUPPORTED),
+    (dict(lda=1 << 41), UNSUPPORTED), (dict(lda=1 << 28), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,status", GEMM8_CASES + [(dict(m=0), OK), (dict(m=-1), INVALID),
+                                                     (dict(ws=P + 8, ws_bytes=1 << 20), UNSUPPORTED)])
+def test_int8_dense(kw, status):
+    assert call(lib.dg_int8_gemm_nt, GEMM8, **kw) == status
+
+
+GEMM8_CONTIGUOUS = dict(a=P, lda=256, sfa=P, sfa_s=1, b=P, ldb=256, b_gs=256 * 64, sfb=P, sfb_s=1, sfb_gs=64, d=P, out=1,
+                        ldd=64, m_indices=P, m=256, n=64, k=256, groups=2, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", GEMM8_CASES + [
+    (dict(m=0), OK), (dict(m=200), MISALIGNED), (dict(groups=0), INVALID), (dict(m_indices=None), INVALID),
+    (dict(b_gs=-16), INVALID), (dict(b_gs=8), UNSUPPORTED), (dict(m_indices=P + 2), UNSUPPORTED)])
+def test_int8_contiguous(kw, status):
+    assert call(lib.dg_m_grouped_int8_gemm_nt_contiguous, GEMM8_CONTIGUOUS, **kw) == status
+
+
+GEMM8_MASKED = dict(a=P, lda=256, a_gs=256 * 32, sfa=P, sfa_s=1, sfa_gs=32, b=P, ldb=256, b_gs=256 * 64, sfb=P, sfb_s=1,
+                    sfb_gs=64, d=P, out=1, ldd=64, d_gs=64 * 32, masked_m=P, groups=2, m=32, n=64, k=256, hint=16,
+                    stream=None)
+
+
+@pytest.mark.parametrize("kw,status", GEMM8_CASES + [
+    (dict(m=0), OK), (dict(groups=0), INVALID), (dict(masked_m=None), INVALID), (dict(d_gs=-1), INVALID),
+    (dict(groups=1025), UNSUPPORTED), (dict(a_gs=8), UNSUPPORTED), (dict(d_gs=1 << 41), UNSUPPORTED)])
+def test_int8_masked(kw, status):
+    assert call(lib.dg_m_grouped_int8_gemm_nt_masked, GEMM8_MASKED, **kw) == status
+
+
 def test_binding_rejects_wrong_tensors():
     """Host tensors, and types, before any library call."""
     x, i = torch.zeros((4, 256)), torch.zeros((4, 2), dtype=torch.int32)
     for f in (lambda: dg.route_topk(x, 2), lambda: dg.route_topk_grad(x, i, x), lambda: dg.combine(x, i),
               lambda: dg.expert_layout_contiguous(i, 8), lambda: dg.expert_layout_masked(i, 8, 4),
               lambda: dg.dispatch_cast_fp8(x, i, rows=8), lambda: dg.dispatch_cast_int8(x, i, rows=8),
-              lambda: dg.combine_grad(x, x, i, i, x)):
+              lambda: dg.combine_grad(x, x, i, i, x), lambda: dg.per_token_cast_int8(x),
+              lambda: dg.int8_gemm_nt((i, x), (i, x), x)):
         with pytest.raises(TypeError):
             f()
 
