@@ -623,7 +623,7 @@ dg_status dg_expert_layout_contiguous(const int32_t* indices, int64_t ldi, int64
  * multiple of 128); 0 for sizes outside the limits. */
 int64_t dg_expert_layout_rows(int64_t tokens, int topk, int experts);
 
-/* Workspace bytes of the two layout calls: 0 up to 4096 slots. */
+/* Workspace bytes of the two layout calls: 0 up to 1024 slots. */
 size_t dg_expert_layout_workspace_size(int64_t tokens, int topk, int experts);
 
 /*

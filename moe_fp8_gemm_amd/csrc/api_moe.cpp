@@ -69,7 +69,7 @@ dg_status layout(const int32_t* indices, int64_t ldi, int64_t tokens, int topk, 
   p.max_m = max_m; p.rows = rows;
   p.m_indices = m_indices; p.row_slot = row_slot; p.slot_row = slot_row; p.counts = counts;
   p.hist = static_cast<int32_t*>(ws);
-  p.blocks = (int)ceil_div(p.slots, kLayoutSlots);
+  p.blocks = p.slots > 0 ? (int)ceil_div(p.slots, layout_block_slots(p.slots)) : 1;
   return of(launch_layout(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -121,8 +121,9 @@ DG_EXPORT int64_t dg_expert_layout_rows(int64_t tokens, int topk, int experts) {
 }
 
 DG_EXPORT size_t dg_expert_layout_workspace_size(int64_t tokens, int topk, int experts) {
-  if (!layout_sizes_ok(tokens, topk, experts) || tokens * topk <= kLayoutSlots) return 0;
-  return (size_t)ceil_div(tokens * topk, kLayoutSlots) * experts * sizeof(int32_t);
+  if (!layout_sizes_ok(tokens, topk, experts)) return 0;
+  const int64_t blocks = ceil_div(tokens * topk, layout_block_slots(tokens * topk));
+  return blocks > 1 ? (size_t)blocks * experts * sizeof(int32_t) : 0;
 }
 
 DG_EXPORT dg_status dg_expert_layout_contiguous(const int32_t* indices, int64_t ldi, int64_t tokens, int topk,

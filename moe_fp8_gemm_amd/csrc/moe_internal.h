@@ -62,8 +62,9 @@ struct LayoutParams {
   int32_t* hist;                  // [blocks, experts]: workspace of large calls
   int blocks;                     // workgroups that share the slots
 };
-// Slots of one workgroup; calls of at most this many need no workspace.
-constexpr int kLayoutSlots = 4096;
+// Slots of one workgroup: 1024 each, so that the work spreads; past 64 workgroups
+// 4096, so that the counts each of them adds up stay few.
+constexpr int64_t layout_block_slots(int64_t slots) { return slots <= 65536 ? 1024 : 4096; }
 
 // Cast of token rows into expert rows, and the plain int8 cast (slot_row null: row t).
 struct DispatchParams {

@@ -9,12 +9,14 @@
 // the order in which workgroups or atomics run.
 //
 // Little is read and written (12 bytes a slot, 8 a row), so the time is launches
-// and dependent steps.  Up to 4096 slots one launch does it all: every workgroup
+// and dependent steps.  Up to 1024 slots one launch does it all: every workgroup
 // counts all slots by itself, the first writes the slots' rows, and all share the
-// rows that hold nothing.  Beyond, a first launch counts each workgroup's 4096
-// slots per expert, and in the second each workgroup adds up the counts before its
+// rows that hold nothing.  Beyond, a first launch counts each workgroup's slots
+// per expert, and in the second each workgroup adds up the counts before its
 // own.  Inside a workgroup each wave ranks its consecutive slots 64 at a time
 // with ballots over the bits of the expert number.
+// Measured, 256 experts, top 8: 64 tokens 4.8 us (one launch), 512 tokens 8.0 us,
+// 4096 tokens 8.7 us, 32768 tokens 16 us.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -23,22 +25,26 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kSteps = kLayoutSlots / kThreads;   // runs of 64 slots of a wave
 static_assert(kThreads >= kMaxExperts, "one thread for each expert");
 
 // Expert of slot s, -1 for none.
 __device__ __forceinline__ int expert_at(const LayoutParams& p, int64_t s) {
   if (s >= p.slots) return -1;
-  const int64_t t = s / p.topk;
-  const int e = p.indices[t * p.ldi + (s - t * p.topk)];
+  int64_t at = s;
+  if (p.ldi != p.topk) {   // slots are below 2^30: 32-bit division
+    const uint32_t t = (uint32_t)s / (uint32_t)p.topk;
+    at = t * p.ldi + ((uint32_t)s - t * p.topk);
+  }
+  const int e = p.indices[at];
   return e >= 0 && e < p.experts ? e : -1;
 }
 
+template <int kSteps>
 __global__ void __launch_bounds__(kThreads) layout_count_kernel(LayoutParams p) {
   __shared__ int count[kMaxExperts];
   count[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t s0 = (int64_t)blockIdx.x * kLayoutSlots;
+  const int64_t s0 = (int64_t)blockIdx.x * (kSteps * kThreads);
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int e = expert_at(p, s0 + i * kThreads + threadIdx.x);
@@ -50,7 +56,8 @@ __global__ void __launch_bounds__(kThreads) layout_count_kernel(LayoutParams p) 
 
 // kCounted: layout_count_kernel has filled p.hist, and each workgroup places its
 // own slots; otherwise every workgroup counts all slots and the first places them.
-template <bool kCounted, int kExperts>
+// kSteps: runs of 64 slots of a wave.
+template <bool kCounted, int kExperts, int kSteps>
 __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) {
   __shared__ int wave_count[kWaves][kExperts];   // slots of an expert in each wave; then the row of the wave's first
   __shared__ int wave_sum[kWaves];
@@ -64,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
   __syncthreads();
 
   // ---- rank each slot among its wave's slots of the same expert
-  const int64_t s0 = (kCounted ? (int64_t)blockIdx.x * kLayoutSlots : 0) + wave * (kSteps * 64);
+  const int64_t s0 = (kCounted ? (int64_t)blockIdx.x * (kSteps * kThreads) : 0) + wave * (kSteps * 64);
   const int bits = 32 - __builtin_clz(p.experts);   // experts <= 2^bits - 1
   int expert[kSteps], rank[kSteps];
 #pragma unroll
@@ -94,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
   int mine = 0, earlier = 0;   // of expert e_mine: all slots, slots of earlier workgroups
   if (e_mine < p.experts) {
     if constexpr (kCounted) {
+#pragma unroll 8
       for (int b = 0; b < p.blocks; ++b) {
         const int c = p.hist[(int64_t)b * p.experts + e_mine];
         mine += c;
@@ -173,30 +181,35 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
       clear(r);
 }
 
-template <bool kCounted>
+template <bool kCounted, int kSteps>
 void place(const LayoutParams& p, int grid, hipStream_t stream) {
   if (p.experts <= 256) {
-    hipLaunchKernelGGL((layout_place_kernel<kCounted, 256>), dim3(grid), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((layout_place_kernel<kCounted, 256, kSteps>), dim3(grid), dim3(kThreads), 0, stream, p);
   } else {
-    hipLaunchKernelGGL((layout_place_kernel<kCounted, kMaxExperts>), dim3(grid), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((layout_place_kernel<kCounted, kMaxExperts, kSteps>), dim3(grid), dim3(kThreads), 0, stream, p);
   }
+}
+
+template <int kSteps>
+hipError_t count_and_place(const LayoutParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((layout_count_kernel<kSteps>), dim3(p.blocks), dim3(kThreads), 0, stream, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  place<true, kSteps>(p, p.blocks, stream);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
-  if (p.slots <= kLayoutSlots) {
+  if (p.blocks == 1) {
     // one workgroup for each 4096 rows, which they share the clearing of
     int64_t grid = (p.rows + 4095) / 4096;
     grid = grid < 1 ? 1 : grid > 64 ? 64 : grid;
-    place<false>(p, (int)grid, stream);
+    place<false, 1>(p, (int)grid, stream);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(layout_count_kernel, dim3(p.blocks), dim3(kThreads), 0, stream, p);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  place<true>(p, p.blocks, stream);
-  return hipGetLastError();
+  return layout_block_slots(p.slots) == kThreads ? count_and_place<1>(p, stream) : count_and_place<4>(p, stream);
 }
 
 }  // namespace dgfp8

@@ -61,7 +61,7 @@ BIG = dict(tokens=1000)   # 8000 slots: needs a workspace
     (dict(topk=0), INVALID), (dict(experts=0), INVALID), (dict(rows=-128), INVALID), (dict(rows=1000), MISALIGNED),
     (dict(experts=1025), UNSUPPORTED), (dict(topk=65, ldi=65), UNSUPPORTED), (dict(tokens=1 << 28), UNSUPPORTED),
     (dict(rows=1 << 31), UNSUPPORTED), (dict(indices=P + 1), UNSUPPORTED), (dict(counts=P + 2), UNSUPPORTED),
-    (BIG, INVALID), (dict(BIG, ws=P, ws_bytes=2 * 64 * 4 - 1), INVALID), (dict(BIG, ws=P + 4, ws_bytes=512), UNSUPPORTED)])
+    (BIG, INVALID), (dict(BIG, ws=P, ws_bytes=8 * 64 * 4 - 1), INVALID), (dict(BIG, ws=P + 4, ws_bytes=4096), UNSUPPORTED)])
 def test_layout_contiguous(kw, status):
     assert call(lib.dg_expert_layout_contiguous, CONTIGUOUS, **kw) == status
 
@@ -81,8 +81,10 @@ def test_layout_sizes():
     assert dg.expert_layout_rows(1, 8, 256) == 8 * 128 and dg.expert_layout_rows(0, 8, 256) == 0
     assert dg.expert_layout_rows(4096, 8, 1) == 32768 // 128 * 128
     assert dg.expert_layout_rows(-1, 8, 256) == 0 and dg.expert_layout_rows(1, 65, 256) == 0
-    assert lib.dg_expert_layout_workspace_size(512, 8, 256) == 0
-    assert lib.dg_expert_layout_workspace_size(513, 8, 256) == 2 * 256 * 4
+    assert lib.dg_expert_layout_workspace_size(128, 8, 256) == 0
+    assert lib.dg_expert_layout_workspace_size(129, 8, 256) == 2 * 256 * 4
+    assert lib.dg_expert_layout_workspace_size(513, 8, 256) == 5 * 256 * 4
+    assert lib.dg_expert_layout_workspace_size(8193, 8, 256) == 17 * 256 * 4
 
 
 DISPATCH = dict(x=P, dtype=1, ldx=256, slot_row=P, lds=2, q=P, ldq=256, sf=P, sf_sm=2, sf_sk=1, tokens=4, topk=2, rows=8,
