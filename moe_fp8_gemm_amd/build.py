@@ -27,8 +27,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdgfp8.so")
-SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "gemm_int8.hip", "cast_fp8.hip", "scratch.hip", "moe_route.hip",
-           "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip"]
+SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "gemm_int8.hip", "gemm_int8_rows.hip", "cast_fp8.hip",
+           "scratch.hip", "moe_route.hip", "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip"]
 ARCH = "gfx950"
 
 

@@ -696,6 +696,9 @@ dg_status check_int8(const void* a, int64_t lda, const float* sfa, int64_t sfa_s
   return DG_SUCCESS;
 }
 
+// Few rows stream B straight into registers (gemm_int8_rows.hip), unless a plan is forced.
+bool int8_by_rows(int64_t m) { return m <= kInt8Rows && g_dense_inst < 0; }
+
 GemmParams int8_params(const void* a, int64_t lda, const float* sfa, int64_t sfa_s, const void* b, int64_t ldb,
                        const float* sfb, int64_t sfb_s, void* d, int64_t ldd, int64_t d_group_stride, int out_dtype,
                        int64_t m, int64_t n, int64_t k, int num_groups) {
@@ -716,7 +719,7 @@ GemmParams int8_params(const void* a, int64_t lda, const float* sfa, int64_t sfa
 }  // namespace
 
 DG_EXPORT size_t dg_int8_gemm_nt_workspace_size(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0 || k % 16 != 0 || !dims_ok(m, n, k)) return 0;
+  if (m <= 0 || n <= 0 || k <= 0 || k % 16 != 0 || !dims_ok(m, n, k) || int8_by_rows(m)) return 0;
   return (size_t)plan_workspace_bytes(plan_dense(m, n, k, hw_cus(), true));
 }
 
@@ -729,8 +732,10 @@ DG_EXPORT dg_status dg_int8_gemm_nt(const void* a, int64_t lda, const float* sfa
   if (st != DG_SUCCESS) return st;
   if (!offsets_fit(m, lda, n, ldb)) return DG_ERROR_NOT_SUPPORTED;
   if (ws && !aligned(ws, 16)) return DG_ERROR_NOT_SUPPORTED;
-  return run_dense(int8_params(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, 0, out_dtype, m, n, k, 1), ws, ws_bytes,
-                   stream);
+  const GemmParams p = int8_params(a, lda, sfa, sfa_s, b, ldb, sfb, sfb_s, d, ldd, 0, out_dtype, m, n, k, 1);
+  if (int8_by_rows(m))
+    return launch_gemm_int8_rows(p, static_cast<hipStream_t>(stream)) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+  return run_dense(p, ws, ws_bytes, stream);
 }
 
 DG_EXPORT size_t dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(int64_t m_total, int64_t n, int64_t k,

@@ -85,6 +85,10 @@ hipError_t launch_gemm(GemmInstance inst, Variant v, const GemmParams& p, int gr
 // The int8 instances (p.int8): the same tiles and variants.
 hipError_t launch_gemm_int8(GemmInstance inst, Variant v, const GemmParams& p, int grid, hipStream_t stream);
 
+// int8 dense GEMM of at most kInt8Rows rows.
+constexpr int64_t kInt8Rows = 8;
+hipError_t launch_gemm_int8_rows(const GemmParams& p, hipStream_t stream);
+
 struct CastParams {
   const void* x;
   int64_t ldx;

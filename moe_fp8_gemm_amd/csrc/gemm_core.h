@@ -90,7 +90,7 @@ struct SfCfg : Base {
 // two v_mfma_i32_16x16x64_i8 on the same fragments (any pairing of K positions
 // that A and B share serves an exact sum), at the rate of one FP8 MFMA of the
 // block.  No scale moves through the K loop.  A K block cut short by the end of K
-// (k % 128 != 0) runs once per tile outside the pipeline, zero-filled.
+// (k % 128 != 0) runs once per tile outside the pipeline (short_block).
 template <class Base>
 struct Int8Cfg : Base {
   static constexpr bool kInt8 = true;
@@ -412,10 +412,46 @@ __device__ __forceinline__ void tile_dma(const TileSrc<C>& t, int kblocks, int w
 }
 
 // int8: the K block that the end of K cuts short (kb, of which k_left < 128 are
-// real).  Rows come through registers, zero-filled past the end, into stage 0; the
-// pipeline is drained before (every DMA landed, every wave done with the stages).
+// real, a multiple of 16).  It is multiplied first, while the pipeline's first
+// blocks are on their way: every lane loads its own fragments from memory,
+// without LDS or a barrier.  m0, n0: first row and column of
+// this wave; rows and columns past the last repeat it.
+template <class C>
+__device__ __forceinline__ void short_block(const TileSrc<C>& t, const GemmParams& p, Acc<C> (&acc)[C::MS][C::NS],
+                                            int kb, int k_left, int64_t m0, int64_t n0, int r16, int q) {
+  BlockRegs<C> r;
+  const uint8_t* a_base = t.a_base + (int64_t)kb * kKBlock;
+  const uint8_t* b_base = t.b_base + (int64_t)kb * kKBlock;
+  // this lane's two 16-byte pieces; one past the end of K reads the row's first
+  // piece instead, and only A's is cleared: a zero in A silences what B holds there
+  const bool in0 = q * 32 < k_left, in1 = q * 32 + 16 < k_left;
+  const uint32_t o0 = in0 ? q * 32 : 0, o1 = in1 ? q * 32 + 16 : 0;
+  auto fragment = [&](const uint8_t* base, int64_t row, int64_t ld) -> i32x8 {
+    const uint32_t off = (uint32_t)(row * ld);
+    const i32x4 lo = *(const i32x4*)(base + (off + o0)), hi = *(const i32x4*)(base + (off + o1));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+#pragma unroll
+  for (int ms = 0; ms < C::MS; ++ms) {
+    const int64_t row = m0 + ms * 16 + r16;
+    r.af[ms] = fragment(a_base, row < p.m ? row : p.m - 1, p.lda);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.af[ms][i] = (i < 4 ? in0 : in1) ? r.af[ms][i] : 0;
+  }
+  static_for<0, C::NS>([&](auto tc) {
+    constexpr int T = decltype(tc)::value;
+    // the column whose B row fragment T holds at r16 (see the B rows' order in decode)
+    const int64_t col = n0 + 32 * (T / 2) + 8 * (r16 / 4) + 4 * (T % 2) + r16 % 4;
+    r.bf[T % C::kBBuf] = fragment(b_base, col < p.n ? col : p.n - 1, p.ldb);
+    static_for<0, C::MS>([&](auto mc) { mfma_one<C, T * C::MS + decltype(mc)::value>(acc, r); });
+  });
+}
+
+// The same for the tiles whose accumulators leave no registers for that (256 and
+// 192 rows): a last step through LDS stage 0, once the pipeline is drained (every
+// DMA landed, every wave done with the stages), zero-filled past the end of K.
 template <class C, int V>
-__device__ __forceinline__ void short_block(const TileSrc<C>& t, Acc<C> (&acc)[C::MS][C::NS], BlockRegs<C>& r, int kb,
+__device__ __forceinline__ void short_block_lds(const TileSrc<C>& t, Acc<C> (&acc)[C::MS][C::NS], BlockRegs<C>& r, int kb,
                                             int k_left, int wave, int lane, uint32_t off0, uint32_t off1, int wr,
                                             int wc, bool compute) {
   constexpr int NA = C::kAChunksPerWave, NB = C::kBChunksPerWave;
@@ -898,6 +934,12 @@ gemm_kernel(GemmParams p) {
 
     // ---- main loop over K blocks, LDS stage = kb % kStages.  A wave none of
     // whose rows is written only keeps the DMA and barrier schedule.
+    constexpr bool kShortFirst = C::kInt8 && C::kMfmas < 24;
+    constexpr bool kShortLast = C::kInt8 && !kShortFirst;
+    if constexpr (kShortFirst)
+      if (cur.k_left && __builtin_amdgcn_ballot_w64(cur.okmask != 0) != 0)
+        short_block<C>(cur.src, p, acc, cur.kbs, cur.k_left, (int64_t)cur.m0 + wr * C::WM,
+                       (int64_t)cur.nt * C::BN + wc * C::WN, r16, q);
     tile_wait<C>();
     int st = 0;
     if (__builtin_amdgcn_ballot_w64(cur.okmask != 0) != 0) {
@@ -908,19 +950,19 @@ gemm_kernel(GemmParams p) {
         step<C, V>(cur.src, acc, mant, r, kb, st, cur.kbs, wave, lane, off0, off1, wr, wc, r16);
         st = st + 1 == C::kStages ? 0 : st + 1;
       }
-      if constexpr (C::kInt8)
+      if constexpr (kShortLast)
         if (cur.k_left)
-          short_block<C, V>(cur.src, acc, r, cur.kbs, cur.k_left, wave, lane, off0, off1, wr, wc, true);
+          short_block_lds<C, V>(cur.src, acc, r, cur.kbs, cur.k_left, wave, lane, off0, off1, wr, wc, true);
     } else {
 #pragma nounroll
       for (int kb = 0; kb < cur.kbs; ++kb) {
         idle_step<C, V>(cur.src, kb, st, cur.kbs, wave, lane);
         st = st + 1 == C::kStages ? 0 : st + 1;
       }
-      if constexpr (C::kInt8) {
+      if constexpr (kShortLast) {
         BlockRegs<C> r;
         if (cur.k_left)
-          short_block<C, V>(cur.src, acc, r, cur.kbs, cur.k_left, wave, lane, off0, off1, wr, wc, false);
+          short_block_lds<C, V>(cur.src, acc, r, cur.kbs, cur.k_left, wave, lane, off0, off1, wr, wc, false);
       }
     }
 
