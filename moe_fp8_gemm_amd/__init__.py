@@ -124,7 +124,8 @@ def _check(status: int, where: str) -> None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the handle alone: building a torch.cuda.Stream object around it costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _codes(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -205,7 +206,7 @@ def _auto_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     # allocated (and zero-filled) on the stream that uses it, so the caching
     # allocator hands its memory to no other stream while that one may use it.
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    key = (idx, torch.cuda.current_stream(idx).cuda_stream)
+    key = (idx, torch._C._cuda_getCurrentRawStream(idx))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)

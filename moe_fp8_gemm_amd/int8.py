@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _AUTO, _check, _stream, _workspace_arg, lib
-from .moe import _DTYPES, _device, _ld, _out, _same_device
+from .moe import _DTYPES, _codes8, _device, _ld, _same_device
 
 Pair = Tuple[torch.Tensor, torch.Tensor]
 
@@ -40,15 +40,18 @@ def _rows(t: torch.Tensor) -> int:
 
 
 def per_token_cast_int8(x: torch.Tensor, q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None) -> Pair:
-    """x bf16 or fp32 [m, k] -> (int8 codes [m, k], fp32 scales [m]): s = max(amax, 1e-4) / 127, q = round(x / s)."""
+    """x bf16 or fp32 [m, k] -> (int8 codes [m, k], fp32 scales [m]): s = max(amax, 1e-4) / 127, q = round(x / s).
+
+    Codes allocated here have rows that begin at 128-byte lines (a row stride above k where k is no multiple of 128);
+    weights laid out once are best kept that way too."""
     _device(x, "x", (torch.bfloat16, torch.float32), 2)
     m, k = x.shape
-    q = _out(q, (m, k), torch.int8, x, "q")
+    q = _codes8(q, m, k, x)
     if sf is None:
         sf = torch.empty(m, dtype=torch.float32, device=x.device)
     if sf.dtype != torch.float32 or not sf.is_cuda or tuple(sf.shape) != (m,):
         raise ValueError(f"sf must be an fp32 device tensor of shape {(m,)}")
-    _same_device(x, q=q, sf=sf)
+    _same_device(x, q, sf)
     _check(lib.dg_per_token_cast_int8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), q.data_ptr(), _ld(q), sf.data_ptr(),
                                       sf.stride(0), m, k, _stream()), "dg_per_token_cast_int8")
     return q, sf
@@ -65,7 +68,7 @@ def int8_gemm_nt(a: Pair, b: Pair, d: torch.Tensor, workspace=_AUTO) -> torch.Te
     if qb.shape[1] != k:
         raise ValueError(f"a has {k} columns, b has {qb.shape[1]}")
     _result(d, (m, n))
-    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d)
+    _same_device(qa, sa, qb, sb, d)
     ws_ptr, ws_bytes = _workspace_arg(workspace, d.device, int(lib.dg_int8_gemm_nt_workspace_size(m, n, k)))
     _check(lib.dg_int8_gemm_nt(qa.data_ptr(), _ld(qa), sa.data_ptr(), sa.stride(0), qb.data_ptr(), _ld(qb),
                                sb.data_ptr(), sb.stride(0), d.data_ptr(), _DTYPES[d.dtype], _ld(d), m, n, k,
@@ -85,7 +88,7 @@ def m_grouped_int8_gemm_nt_contiguous(a: Pair, b: Pair, d: torch.Tensor, m_indic
     _device(m_indices, "m_indices", (torch.int32,), 1)
     if m_indices.shape[0] != m:
         raise ValueError(f"m_indices must have {m} elements, got {m_indices.shape[0]}")
-    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d, m_indices=m_indices)
+    _same_device(qa, sa, qb, sb, d, m_indices)
     need = int(lib.dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(m, n, k, g))
     ws_ptr, ws_bytes = _workspace_arg(workspace, d.device, need)
     _check(lib.dg_m_grouped_int8_gemm_nt_contiguous(
@@ -107,7 +110,7 @@ def m_grouped_int8_gemm_nt_masked(a: Pair, b: Pair, d: torch.Tensor, masked_m: t
     _device(masked_m, "masked_m", (torch.int32,), 1)
     if masked_m.shape[0] != g:
         raise ValueError(f"masked_m must have {g} elements, got {masked_m.shape[0]}")
-    _same_device(qa, sfa=sa, b=qb, sfb=sb, d=d, masked_m=masked_m)
+    _same_device(qa, sa, qb, sb, d, masked_m)
     _check(lib.dg_m_grouped_int8_gemm_nt_masked(
         qa.data_ptr(), _rows(qa), qa.stride(0), sa.data_ptr(), sa.stride(1), sa.stride(0), qb.data_ptr(), _rows(qb),
         qb.stride(0), sb.data_ptr(), sb.stride(1), sb.stride(0), d.data_ptr(), _DTYPES[d.dtype], _rows(d), d.stride(0),

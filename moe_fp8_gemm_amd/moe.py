@@ -38,26 +38,35 @@ class ExpertLayout(NamedTuple):
         return self.row_slot.shape[0]
 
 
-def _device(t: torch.Tensor, name: str, dtypes, dim: int) -> torch.Tensor:
+def _refuse(t: torch.Tensor, name: str, dtypes, dim: int) -> None:
     if t.dtype not in dtypes or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor of type {' or '.join(str(d) for d in dtypes)}, "
                         f"got {t.dtype} on {t.device}")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    if t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.numel() > 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
+
+
+# The checks below run on every call, and a small call costs little more than they
+# do: one expression for the usual case, and the reason is worked out on refusal.
+def _device(t: torch.Tensor, name: str, dtypes, dim: int) -> torch.Tensor:
+    if t.dtype not in dtypes or not t.is_cuda or t.dim() != dim or t.stride(-1) != 1:
+        _refuse(t, name, dtypes, dim)
     return t
 
 
 def _ld(t: torch.Tensor) -> int:
     """Row stride; a matrix of at most one row may carry any."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, the first on {first.device}")
 
 
 def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
@@ -67,6 +76,14 @@ def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _codes8(q: Optional[torch.Tensor], rows: int, k: int, like: torch.Tensor) -> torch.Tensor:
+    """int8 codes [rows, k]; allocated here, rows begin at 128-byte lines, which the GEMM reads up to a third faster than
+    rows that straddle them."""
+    if q is not None or k % 128 == 0:
+        return _out(q, (rows, k), torch.int8, like, "q")
+    return torch.empty((rows, (k + 127) // 128 * 128), dtype=torch.int8, device=like.device)[:, :k]
 
 
 def _score(score: str) -> int:
@@ -99,7 +116,7 @@ def route_topk(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias:
             raise ValueError(f"bias must have {e} elements, got {bias.shape[0]}")
     indices = _out(indices, (t, topk), torch.int32, logits, "indices")
     weights = _out(weights, (t, topk), torch.float32, logits, "weights")
-    _same_device(logits, bias=bias, indices=indices, weights=weights)
+    _same_device(logits, bias, indices, weights)
     _check(lib.dg_route_topk(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
                              None if bias is None else bias.data_ptr(), indices.data_ptr(), _ld(indices),
                              weights.data_ptr(), _ld(weights), t, e, topk, num_expert_groups, topk_groups,
@@ -123,7 +140,7 @@ def route_topk_grad(logits: torch.Tensor, indices: torch.Tensor, dweights: torch
     if indices.shape[0] != t or indices.shape != dweights.shape:
         raise ValueError(f"indices {tuple(indices.shape)} and dweights {tuple(dweights.shape)} must be [{t}, topk]")
     dlogits = _out(dlogits, (t, e), logits.dtype, logits, "dlogits")
-    _same_device(logits, indices=indices, dweights=dweights, dlogits=dlogits)
+    _same_device(logits, indices, dweights, dlogits)
     _check(lib.dg_route_topk_grad(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits), indices.data_ptr(),
                                   _ld(indices), dweights.data_ptr(), _ld(dweights), dlogits.data_ptr(), _ld(dlogits),
                                   t, e, indices.shape[1], _score(score), bool(renormalize), scale, _stream()),
@@ -136,11 +153,16 @@ def expert_layout_rows(tokens: int, topk: int, num_experts: int) -> int:
     return int(lib.dg_expert_layout_rows(int(tokens), int(topk), int(num_experts)))
 
 
-def _layout_workspace(indices: torch.Tensor, num_experts: int) -> Optional[torch.Tensor]:
-    if indices.numel() <= 4096:
-        return None
-    n = int(lib.dg_expert_layout_workspace_size(indices.shape[0], indices.shape[1], num_experts))
-    return torch.empty(n, dtype=torch.uint8, device=indices.device) if n else None
+def _layout_buffers(indices: torch.Tensor, num_experts: int, m_rows: int, rows: int):
+    """m_indices, row_slot, slot_row, counts and the workspace (or None), as parts of one allocation."""
+    t, k = indices.shape
+    sizes = [max(m_rows, 0), max(rows, 0), t * k, max(num_experts, 0)]
+    n = lib.dg_expert_layout_workspace_size(t, k, num_experts) // 4
+    if n:
+        sizes.append(-sum(sizes) % 4)                    # the workspace begins at a 16-byte boundary
+        sizes.append(n)
+    parts = torch.empty(sum(sizes), dtype=torch.int32, device=indices.device).split(sizes)
+    return parts[0], parts[1], parts[2].view(t, k), parts[3], parts[5] if n else None
 
 
 def expert_layout_contiguous(indices: torch.Tensor, num_experts: int, rows: Optional[int] = None) -> ExpertLayout:
@@ -154,16 +176,11 @@ def expert_layout_contiguous(indices: torch.Tensor, num_experts: int, rows: Opti
     t, k = indices.shape
     if rows is None:
         rows = expert_layout_rows(t, k, num_experts)
-    dev = indices.device
-    m_indices = torch.empty(rows, dtype=torch.int32, device=dev)
-    row_slot = torch.empty(rows, dtype=torch.int32, device=dev)
-    slot_row = torch.empty((t, k), dtype=torch.int32, device=dev)
-    counts = torch.empty(max(num_experts, 0), dtype=torch.int32, device=dev)
-    ws = _layout_workspace(indices, num_experts)
+    m_indices, row_slot, slot_row, counts, ws = _layout_buffers(indices, num_experts, rows, rows)
     _check(lib.dg_expert_layout_contiguous(indices.data_ptr(), _ld(indices), t, k, num_experts, rows,
                                            m_indices.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
                                            counts.data_ptr(), None if ws is None else ws.data_ptr(),
-                                           0 if ws is None else ws.numel(), _stream()), "dg_expert_layout_contiguous")
+                                           0 if ws is None else 4 * ws.numel(), _stream()), "dg_expert_layout_contiguous")
     return ExpertLayout(m_indices, row_slot, slot_row, counts)
 
 
@@ -172,14 +189,10 @@ def expert_layout_masked(indices: torch.Tensor, num_experts: int, max_m: int) ->
     tensor seen as [experts * max_m, ...]); slots past max_m are dropped.  ``counts`` is the GEMM's masked_m."""
     _device(indices, "indices", (torch.int32,), 2)
     t, k = indices.shape
-    dev = indices.device
-    row_slot = torch.empty(max(num_experts * max_m, 0), dtype=torch.int32, device=dev)
-    slot_row = torch.empty((t, k), dtype=torch.int32, device=dev)
-    masked_m = torch.empty(max(num_experts, 0), dtype=torch.int32, device=dev)
-    ws = _layout_workspace(indices, num_experts)
+    _, row_slot, slot_row, masked_m, ws = _layout_buffers(indices, num_experts, 0, num_experts * max_m)
     _check(lib.dg_expert_layout_masked(indices.data_ptr(), _ld(indices), t, k, num_experts, max_m,
                                        masked_m.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
-                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                       None if ws is None else ws.data_ptr(), 0 if ws is None else 4 * ws.numel(),
                                        _stream()), "dg_expert_layout_masked")
     return ExpertLayout(None, row_slot, slot_row, masked_m)
 
@@ -218,7 +231,7 @@ def dispatch_cast_fp8(x: torch.Tensor, slot_row: torch.Tensor, rows: Optional[in
         raise ValueError(f"sf must be an fp32 device tensor of shape {(rows, k // 128)}")
     if q.shape[1] != k:
         raise ValueError(f"q must have {k} columns, got {q.shape[1]}")
-    _same_device(x, slot_row=slot_row, q=q, sf=sf)
+    _same_device(x, slot_row, q, sf)
     _check(lib.dg_dispatch_cast_fp8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), slot_row.data_ptr(), _ld(slot_row),
                                     q.data_ptr(), _ld(q), sf.data_ptr(), sf.stride(0), sf.stride(1), t,
                                     slot_row.shape[1], rows, k, bool(ue8m0), _stream()), "dg_dispatch_cast_fp8")
@@ -230,12 +243,12 @@ def dispatch_cast_int8(x: torch.Tensor, slot_row: torch.Tensor, rows: Optional[i
     """As ``dispatch_cast_fp8`` with the int8 cast: (int8 codes [rows, k], fp32 scales [rows])."""
     rows = _dispatch_args(x, slot_row, rows, q)
     t, k = x.shape
-    q = _out(q, (rows, k), torch.int8, x, "q")
+    q = _codes8(q, rows, k, x)
     if sf is None:
         sf = torch.empty(rows, dtype=torch.float32, device=x.device)
     if sf.dtype != torch.float32 or not sf.is_cuda or tuple(sf.shape) != (rows,):
         raise ValueError(f"sf must be an fp32 device tensor of shape {(rows,)}")
-    _same_device(x, slot_row=slot_row, q=q, sf=sf)
+    _same_device(x, slot_row, q, sf)
     _check(lib.dg_dispatch_cast_int8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), slot_row.data_ptr(), _ld(slot_row),
                                      q.data_ptr(), _ld(q), sf.data_ptr(), sf.stride(0), t, slot_row.shape[1], rows,
                                      k, _stream()), "dg_dispatch_cast_int8")
@@ -262,7 +275,7 @@ def combine(y: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.Ten
     _device(out, "out", (torch.bfloat16, torch.float32), 2)
     if tuple(out.shape) != (t, h):
         raise ValueError(f"out must have shape {(t, h)}, got {tuple(out.shape)}")
-    _same_device(y, slot_row=slot_row, weights=weights, out=out)
+    _same_device(y, slot_row, weights, out)
     _check(lib.dg_combine(y.data_ptr(), _ld(y), slot_row.data_ptr(), _ld(slot_row),
                           None if weights is None else weights.data_ptr(), 0 if weights is None else _ld(weights),
                           out.data_ptr(), _DTYPES[out.dtype], _ld(out), t, k, rows, h, _stream()), "dg_combine")
@@ -289,7 +302,7 @@ def combine_grad(dout: torch.Tensor, y: torch.Tensor, slot_row: torch.Tensor, ro
                          f"{tuple(dout.shape)}, {tuple(weights.shape)} and {tuple(row_slot.shape)}")
     dy = _out(dy, (rows, h), torch.bfloat16, y, "dy")
     dweights = _out(dweights, (t, k), torch.float32, y, "dweights")
-    _same_device(y, dout=dout, slot_row=slot_row, row_slot=row_slot, weights=weights, dy=dy, dweights=dweights)
+    _same_device(y, dout, slot_row, row_slot, weights, dy, dweights)
     _check(lib.dg_combine_grad(dout.data_ptr(), _ld(dout), y.data_ptr(), _ld(y), slot_row.data_ptr(), _ld(slot_row),
                                row_slot.data_ptr(), weights.data_ptr(), _ld(weights), dy.data_ptr(), _ld(dy),
                                dweights.data_ptr(), _ld(dweights), t, k, rows, h, _stream()), "dg_combine_grad")
