@@ -48,18 +48,18 @@ def _refuse(t: torch.Tensor, name: str, dtypes, dim: int) -> None:
         raise ValueError(f"{name} must have unit stride along its last dimension")
 
 
-# The checks below run on every call, and a small call costs little more than they
-# do: one expression for the usual case, and the reason is worked out on refusal.
+# The checks run on every call, and a small call costs little more than they do: one
+# expression for the usual case, and the reason is worked out on refusal.
 def _device(t: torch.Tensor, name: str, dtypes, dim: int) -> torch.Tensor:
-    if t.dtype not in dtypes or not t.is_cuda or t.dim() != dim or t.stride(-1) != 1:
+    if t.dtype not in dtypes or t.get_device() < 0 or t.dim() != dim or t.stride(-1) != 1:
         _refuse(t, name, dtypes, dim)
     return t
 
 
-def _ld(t: torch.Tensor) -> int:
+def _ld(t: torch.Tensor, cols: int) -> int:
     """Row stride; a matrix of at most one row may carry any."""
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    ld = t.stride(0)
+    return ld if ld >= cols or t.shape[0] > 1 else cols
 
 
 def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
@@ -73,7 +73,7 @@ def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str)
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     _device(t, name, (dtype,), len(shape))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -106,7 +106,7 @@ def route_topk(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias:
     bias of -inf takes an expert out; slots without an expert get index -1 and weight 0.  A NaN makes a token's
     weights NaN.
     """
-    _device(logits, "logits", tuple(_DTYPES), 2)
+    _device(logits, "logits", _DTYPES, 2)
     t, e = logits.shape
     if group_score not in ("max", "top2"):
         raise ValueError(f"group_score must be 'max' or 'top2', got {group_score!r}")
@@ -117,9 +117,9 @@ def route_topk(logits: torch.Tensor, topk: int, *, score: str = "softmax", bias:
     indices = _out(indices, (t, topk), torch.int32, logits, "indices")
     weights = _out(weights, (t, topk), torch.float32, logits, "weights")
     _same_device(logits, bias, indices, weights)
-    _check(lib.dg_route_topk(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
-                             None if bias is None else bias.data_ptr(), indices.data_ptr(), _ld(indices),
-                             weights.data_ptr(), _ld(weights), t, e, topk, num_expert_groups, topk_groups,
+    _check(lib.dg_route_topk(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits, e),
+                             None if bias is None else bias.data_ptr(), indices.data_ptr(), _ld(indices, topk),
+                             weights.data_ptr(), _ld(weights, topk), t, e, topk, num_expert_groups, topk_groups,
                              group_score == "top2", _score(score), bool(renormalize), scale, _stream()),
            "dg_route_topk")
     return indices, weights
@@ -133,17 +133,18 @@ def route_topk_grad(logits: torch.Tensor, indices: torch.Tensor, dweights: torch
     indices int32 and dweights fp32 are [tokens, topk]; the other arguments as they were given to ``route_topk``.
     The choice of experts is held fixed, so a bias or groups do not enter.
     """
-    _device(logits, "logits", tuple(_DTYPES), 2)
+    _device(logits, "logits", _DTYPES, 2)
     _device(indices, "indices", (torch.int32,), 2)
     _device(dweights, "dweights", (torch.float32,), 2)
     t, e = logits.shape
+    topk = indices.shape[1]
     if indices.shape[0] != t or indices.shape != dweights.shape:
         raise ValueError(f"indices {tuple(indices.shape)} and dweights {tuple(dweights.shape)} must be [{t}, topk]")
     dlogits = _out(dlogits, (t, e), logits.dtype, logits, "dlogits")
     _same_device(logits, indices, dweights, dlogits)
-    _check(lib.dg_route_topk_grad(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits), indices.data_ptr(),
-                                  _ld(indices), dweights.data_ptr(), _ld(dweights), dlogits.data_ptr(), _ld(dlogits),
-                                  t, e, indices.shape[1], _score(score), bool(renormalize), scale, _stream()),
+    _check(lib.dg_route_topk_grad(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits, e), indices.data_ptr(),
+                                  _ld(indices, topk), dweights.data_ptr(), _ld(dweights, topk), dlogits.data_ptr(), _ld(dlogits, e),
+                                  t, e, topk, _score(score), bool(renormalize), scale, _stream()),
            "dg_route_topk_grad")
     return dlogits
 
@@ -177,7 +178,7 @@ def expert_layout_contiguous(indices: torch.Tensor, num_experts: int, rows: Opti
     if rows is None:
         rows = expert_layout_rows(t, k, num_experts)
     m_indices, row_slot, slot_row, counts, ws = _layout_buffers(indices, num_experts, rows, rows)
-    _check(lib.dg_expert_layout_contiguous(indices.data_ptr(), _ld(indices), t, k, num_experts, rows,
+    _check(lib.dg_expert_layout_contiguous(indices.data_ptr(), _ld(indices, k), t, k, num_experts, rows,
                                            m_indices.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
                                            counts.data_ptr(), None if ws is None else ws.data_ptr(),
                                            0 if ws is None else 4 * ws.numel(), _stream()), "dg_expert_layout_contiguous")
@@ -190,7 +191,7 @@ def expert_layout_masked(indices: torch.Tensor, num_experts: int, max_m: int) ->
     _device(indices, "indices", (torch.int32,), 2)
     t, k = indices.shape
     _, row_slot, slot_row, masked_m, ws = _layout_buffers(indices, num_experts, 0, num_experts * max_m)
-    _check(lib.dg_expert_layout_masked(indices.data_ptr(), _ld(indices), t, k, num_experts, max_m,
+    _check(lib.dg_expert_layout_masked(indices.data_ptr(), _ld(indices, k), t, k, num_experts, max_m,
                                        masked_m.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
                                        None if ws is None else ws.data_ptr(), 0 if ws is None else 4 * ws.numel(),
                                        _stream()), "dg_expert_layout_masked")
@@ -221,7 +222,7 @@ def dispatch_cast_fp8(x: torch.Tensor, slot_row: torch.Tensor, rows: Optional[in
     another along the rows, as the GEMMs read them best.
     """
     rows = _dispatch_args(x, slot_row, rows, q)
-    t, k = x.shape
+    (t, k), topk = x.shape, slot_row.shape[1]
     if q is None:
         q = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=x.device)
     if sf is None:
@@ -232,9 +233,9 @@ def dispatch_cast_fp8(x: torch.Tensor, slot_row: torch.Tensor, rows: Optional[in
     if q.shape[1] != k:
         raise ValueError(f"q must have {k} columns, got {q.shape[1]}")
     _same_device(x, slot_row, q, sf)
-    _check(lib.dg_dispatch_cast_fp8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), slot_row.data_ptr(), _ld(slot_row),
-                                    q.data_ptr(), _ld(q), sf.data_ptr(), sf.stride(0), sf.stride(1), t,
-                                    slot_row.shape[1], rows, k, bool(ue8m0), _stream()), "dg_dispatch_cast_fp8")
+    _check(lib.dg_dispatch_cast_fp8(x.data_ptr(), _DTYPES[x.dtype], _ld(x, k), slot_row.data_ptr(), _ld(slot_row, topk),
+                                    q.data_ptr(), _ld(q, k), sf.data_ptr(), sf.stride(0), sf.stride(1), t,
+                                    topk, rows, k, bool(ue8m0), _stream()), "dg_dispatch_cast_fp8")
     return q, sf
 
 
@@ -242,15 +243,15 @@ def dispatch_cast_int8(x: torch.Tensor, slot_row: torch.Tensor, rows: Optional[i
                        q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None):
     """As ``dispatch_cast_fp8`` with the int8 cast: (int8 codes [rows, k], fp32 scales [rows])."""
     rows = _dispatch_args(x, slot_row, rows, q)
-    t, k = x.shape
+    (t, k), topk = x.shape, slot_row.shape[1]
     q = _codes8(q, rows, k, x)
     if sf is None:
         sf = torch.empty(rows, dtype=torch.float32, device=x.device)
     if sf.dtype != torch.float32 or not sf.is_cuda or tuple(sf.shape) != (rows,):
         raise ValueError(f"sf must be an fp32 device tensor of shape {(rows,)}")
     _same_device(x, slot_row, q, sf)
-    _check(lib.dg_dispatch_cast_int8(x.data_ptr(), _DTYPES[x.dtype], _ld(x), slot_row.data_ptr(), _ld(slot_row),
-                                     q.data_ptr(), _ld(q), sf.data_ptr(), sf.stride(0), t, slot_row.shape[1], rows,
+    _check(lib.dg_dispatch_cast_int8(x.data_ptr(), _DTYPES[x.dtype], _ld(x, k), slot_row.data_ptr(), _ld(slot_row, topk),
+                                     q.data_ptr(), _ld(q, k), sf.data_ptr(), sf.stride(0), t, topk, rows,
                                      k, _stream()), "dg_dispatch_cast_int8")
     return q, sf
 
@@ -273,12 +274,12 @@ def combine(y: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.Ten
     if out is None:
         out = torch.empty((t, h), dtype=torch.bfloat16, device=y.device)
     _device(out, "out", (torch.bfloat16, torch.float32), 2)
-    if tuple(out.shape) != (t, h):
+    if out.shape != (t, h):
         raise ValueError(f"out must have shape {(t, h)}, got {tuple(out.shape)}")
     _same_device(y, slot_row, weights, out)
-    _check(lib.dg_combine(y.data_ptr(), _ld(y), slot_row.data_ptr(), _ld(slot_row),
-                          None if weights is None else weights.data_ptr(), 0 if weights is None else _ld(weights),
-                          out.data_ptr(), _DTYPES[out.dtype], _ld(out), t, k, rows, h, _stream()), "dg_combine")
+    _check(lib.dg_combine(y.data_ptr(), _ld(y, h), slot_row.data_ptr(), _ld(slot_row, k),
+                          None if weights is None else weights.data_ptr(), 0 if weights is None else _ld(weights, k),
+                          out.data_ptr(), _DTYPES[out.dtype], _ld(out, h), t, k, rows, h, _stream()), "dg_combine")
     return out
 
 
@@ -297,13 +298,13 @@ def combine_grad(dout: torch.Tensor, y: torch.Tensor, slot_row: torch.Tensor, ro
     _device(weights, "weights", (torch.float32,), 2)
     t, k = slot_row.shape
     rows, h = y.shape
-    if tuple(dout.shape) != (t, h) or weights.shape != slot_row.shape or row_slot.shape[0] != rows:
+    if dout.shape != (t, h) or weights.shape != slot_row.shape or row_slot.shape[0] != rows:
         raise ValueError(f"dout must have shape {(t, h)}, weights {(t, k)} and row_slot {(rows,)}, got "
                          f"{tuple(dout.shape)}, {tuple(weights.shape)} and {tuple(row_slot.shape)}")
     dy = _out(dy, (rows, h), torch.bfloat16, y, "dy")
     dweights = _out(dweights, (t, k), torch.float32, y, "dweights")
     _same_device(y, dout, slot_row, row_slot, weights, dy, dweights)
-    _check(lib.dg_combine_grad(dout.data_ptr(), _ld(dout), y.data_ptr(), _ld(y), slot_row.data_ptr(), _ld(slot_row),
-                               row_slot.data_ptr(), weights.data_ptr(), _ld(weights), dy.data_ptr(), _ld(dy),
-                               dweights.data_ptr(), _ld(dweights), t, k, rows, h, _stream()), "dg_combine_grad")
+    _check(lib.dg_combine_grad(dout.data_ptr(), _ld(dout, h), y.data_ptr(), _ld(y, h), slot_row.data_ptr(), _ld(slot_row, k),
+                               row_slot.data_ptr(), weights.data_ptr(), _ld(weights, k), dy.data_ptr(), _ld(dy, h),
+                               dweights.data_ptr(), _ld(dweights, k), t, k, rows, h, _stream()), "dg_combine_grad")
     return dy, dweights
