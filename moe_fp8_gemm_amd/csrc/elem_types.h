@@ -34,6 +34,15 @@ __device__ __forceinline__ Eight<T> load_eight(const typename T::store* src) {
   for (int i = 0; i < (int)(sizeof(typename T::store) / 2); ++i) v.q[i] = ((const u32x4*)src)[i];
   return v;
 }
+// The same for what is read once: passed through without being kept in L2.
+template <class T>
+__device__ __forceinline__ Eight<T> stream_eight(const typename T::store* src) {
+  Eight<T> v;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(typename T::store) / 2); ++i)
+    v.q[i] = __builtin_nontemporal_load((const u32x4*)src + i);
+  return v;
+}
 template <class T>
 __device__ __forceinline__ Eight<T> zero_eight() {
   Eight<T> v;
@@ -52,6 +61,7 @@ __device__ __forceinline__ void widen_eight(const Eight<T>& v, float (&x)[8]) {
     }
   }
 }
+// Stores pass through as well: the rows moved here exceed L2 many times over.
 template <class T>
 __device__ __forceinline__ void store_eight(typename T::store* dst, const float (&x)[8]) {
   if constexpr (sizeof(typename T::store) == 4) {
@@ -60,14 +70,14 @@ __device__ __forceinline__ void store_eight(typename T::store* dst, const float 
       u32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(x[4 * h + i]);
-      ((u32x4*)dst)[h] = v;
+      __builtin_nontemporal_store(v, (u32x4*)dst + h);
     }
   } else {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       v[i] = (uint32_t)narrow(T{}, x[2 * i]) | ((uint32_t)narrow(T{}, x[2 * i + 1]) << 16);
-    *(u32x4*)dst = v;
+    __builtin_nontemporal_store(v, (u32x4*)dst);
   }
 }
 

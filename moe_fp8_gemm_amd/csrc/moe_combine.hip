@@ -9,7 +9,10 @@
 // Bound by memory: every row is read once (and written once, in the gradient).
 // A thread owns eight columns of a token, and loads a batch of rows before it
 // adds the first, so that several 16-byte loads are in flight a lane.  The row
-// numbers and weights are the same for the whole workgroup.
+// numbers and weights are the same for the whole workgroup.  Rows stream past L2
+// (non-temporal): nothing is used twice.
+// Measured: 4096 tokens of 7168 from 32768 x 0.98 rows (519 MB) 94 us, 5.5 TB/s; its gradient
+// for 8192 tokens, top 4 (1076 MB) 191 us, 5.6 TB/s; through L2 109 and 221 us.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -37,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineParams p) {
       const int64_t r = j0 + b < p.topk ? rows[j0 + b] : -1;
       there[b] = r >= 0 && r < p.rows;
       w[b] = there[b] && ws ? ws[j0 + b] : 1.0f;
-      if (there[b]) v[b] = load_eight<BF16>(y + r * p.ldy);
+      if (there[b]) v[b] = stream_eight<BF16>(y + r * p.ldy);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(CombineGradParam
     for (int64_t r = r0; r < r0 + kClearRows && r < p.rows; ++r) {
       if (p.row_slot[r] >= 0) continue;
       uint16_t* dst = (uint16_t*)p.dy + r * p.lddy;
-      for (int64_t c = threadIdx.x * 8; c < p.h; c += kThreads * 8) *(u32x4*)(dst + c) = (u32x4){0, 0, 0, 0};
+      for (int64_t c = threadIdx.x * 8; c < p.h; c += kThreads * 8) __builtin_nontemporal_store((u32x4){0, 0, 0, 0}, (u32x4*)(dst + c));
     }
     return;
   }
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(CombineGradParam
       Eight<BF16> v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
-        if (row[b] >= 0) v[b] = load_eight<BF16>(y + row[b] * p.ldy + c);
+        if (row[b] >= 0) v[b] = stream_eight<BF16>(y + row[b] * p.ldy + c);
       float gx[8];
       widen_eight(g, gx);
 #pragma unroll
