@@ -63,6 +63,11 @@ __device__ __forceinline__ void dma16(const uint8_t* sbase, uint32_t voff, uint3
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(uniform_ptr(sbase)), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
+// The same past L2 (non-temporal), for operands that one workgroup reads once.
+__device__ __forceinline__ void dma16_stream(const uint8_t* sbase, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+               :: "v"(voff), "s"(uniform_ptr(sbase)), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+}
 __device__ __forceinline__ void dma4(const float* vaddr, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off"
                :: "v"(vaddr), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");

@@ -50,6 +50,7 @@ struct Cfg {
   static constexpr int kOcc = OCC_;         // workgroups resident per CU
   static constexpr bool kPackedSf = false;  // scales: fp32 (false) or packed UE8M0 (see SfCfg)
   static constexpr bool kInt8 = false;      // int8 operands with row and column scales (see Int8Cfg)
+  static constexpr bool kStreamB = false;   // B's loads pass L2 by
   static constexpr int kWaves = WAVES_M * WAVES_N;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -96,6 +97,10 @@ struct Int8Cfg : Base {
   static constexpr bool kInt8 = true;
   static constexpr int kLoadsPerStage = Base::kLoadsPerStage - 1;   // no scales
   static_assert(Base::BM + Base::BN <= Base::kThreads, "one thread fetches each of a tile's scales");
+  // 64-row tiles serve problems of at most 64 rows (a group), so one workgroup
+  // reads a row of B, once.  Masked decode of 16 groups of 4096x7168 (470 MB): 86 us
+  // through L2, 78 us past it; 64x4096x7168 13.2 to 12.6 us.
+  static constexpr bool kStreamB = Base::BM == 64;
 };
 
 // Accumulator of a 16x16 sub-tile.
@@ -143,7 +148,11 @@ __device__ __forceinline__ void issue_dma_part(const TileSrc<C>& t, int kb, int 
     dma16(t.a_base + (int64_t)kb * kKBlock, t.a_off[d], lds_addr(lds_a<C, V>(st)) + (wave * NA + d) * 1024);
   } else if (d < NA + NB) {
     const int j = d - NA;
-    dma16(t.b_base + (int64_t)kb * kKBlock, t.b_off[j], lds_addr(lds_b<C, V>(st)) + (wave * NB + j) * 1024);
+    if constexpr (C::kStreamB) {
+      dma16_stream(t.b_base + (int64_t)kb * kKBlock, t.b_off[j], lds_addr(lds_b<C, V>(st)) + (wave * NB + j) * 1024);
+    } else {
+      dma16(t.b_base + (int64_t)kb * kKBlock, t.b_off[j], lds_addr(lds_b<C, V>(st)) + (wave * NB + j) * 1024);
+    }
   } else {
     // fp32: one word per K block (s_src already points at the unit's first
     // block); packed: one word per 4 K blocks, indexed by the absolute block.
@@ -987,18 +996,24 @@ gemm_kernel(GemmParams p) {
       // device-scope (sc1) buffer accesses, written through to and read from the
       // device-coherent level, which avoids the L2-wide writeback and invalidate
       // that a device-scope fence costs.  The buffer's size bounds every access.
+      //   int8 sums do not depend on their order: the last unit keeps its own partial
+      // in its registers and reads only the others', and waves without a row to
+      // write take no part.
       const int tile_mn = cur.mt * tiles_n + cur.nt;
       constexpr int kTileFloats = C::BM * C::BN;
       const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
           p.ws + (int64_t)tile_mn * splits * kTileFloats, 0, splits * kTileFloats * 4, kRawBufferFlags);
       const int lane_off = ((wave * C::kMfmas) * 64 + lane) * 16;   // bytes, (ms, j) = (0, 0)
+      const bool takes_part = !C::kInt8 || __builtin_amdgcn_ballot_w64(cur.okmask != 0) != 0;
+      if (takes_part) {
 #pragma unroll
-      for (int ms = 0; ms < C::MS; ++ms)
+        for (int ms = 0; ms < C::MS; ++ms)
 #pragma unroll
-        for (int j = 0; j < C::NS; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[ms][j]), part,
-                                                 lane_off + (ms * C::NS + j) * 1024,
-                                                 cur.split * kTileFloats * 4, kScopeDevice);
+          for (int j = 0; j < C::NS; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[ms][j]), part,
+                                                   lane_off + (ms * C::NS + j) * 1024,
+                                                   cur.split * kTileFloats * 4, kScopeDevice);
+      }
       // every partial store has been acknowledged before the arrival is counted
       __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
       __shared__ int last_flag;
@@ -1008,34 +1023,40 @@ gemm_kernel(GemmParams p) {
                     splits - 1;
       __syncthreads();
       if (last_flag) {
+        if constexpr (!C::kInt8) {
 #pragma unroll
-        for (int ms = 0; ms < C::MS; ++ms)
+          for (int ms = 0; ms < C::MS; ++ms)
 #pragma unroll
-          for (int j = 0; j < C::NS; ++j) acc[ms][j] = (Acc<C>){0, 0, 0, 0};
+            for (int j = 0; j < C::NS; ++j) acc[ms][j] = (Acc<C>){0, 0, 0, 0};
+        }
         // Splits in batches: every load of a batch is issued before the first
         // add, so one memory round trip serves the whole batch; the adds then
         // run in split order.
-        constexpr int kBatch = 32 / (C::kMfmas * 4) > 0 ? 32 / (C::kMfmas * 4) : 1;
-        for (int sp0 = 0; sp0 < splits; sp0 += kBatch) {
+        constexpr int kBatchRegs = C::kInt8 ? 64 : 32;
+        constexpr int kBatch = kBatchRegs / (C::kMfmas * 4) > 0 ? kBatchRegs / (C::kMfmas * 4) : 1;
+        const int parts = C::kInt8 ? (takes_part ? splits - 1 : 0) : splits;
+        for (int sp0 = 0; sp0 < parts; sp0 += kBatch) {
           Acc<C> v[kBatch][C::MS][C::NS];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b)
+          for (int b = 0; b < kBatch; ++b) {
+            const int sp = sp0 + b + (C::kInt8 && sp0 + b >= cur.split ? 1 : 0);
 #pragma unroll
             for (int ms = 0; ms < C::MS; ++ms)
 #pragma unroll
               for (int j = 0; j < C::NS; ++j)
-                v[b][ms][j] = sp0 + b < splits
+                v[b][ms][j] = sp0 + b < parts
                                   ? __builtin_bit_cast(Acc<C>, __builtin_amdgcn_raw_buffer_load_b128(
                                                                   part, lane_off + (ms * C::NS + j) * 1024,
-                                                                  (sp0 + b) * kTileFloats * 4, kScopeDevice))
+                                                                  sp * kTileFloats * 4, kScopeDevice))
                                   : (Acc<C>){0, 0, 0, 0};
+          }
 #pragma unroll
           for (int b = 0; b < kBatch; ++b)
 #pragma unroll
             for (int ms = 0; ms < C::MS; ++ms)
 #pragma unroll
               for (int j = 0; j < C::NS; ++j)
-                if (sp0 + b < splits) acc[ms][j] += v[b][ms][j];
+                if (sp0 + b < parts) acc[ms][j] += v[b][ms][j];
         }
         // ready for the next call
         if (threadIdx.x == 0) __hip_atomic_store(p.counters + tile_mn, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
