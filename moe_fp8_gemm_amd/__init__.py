@@ -4,7 +4,9 @@ Argument marshalling only.  Each function checks dtypes/devices, hands raw
 device pointers, strides and torch's current HIP stream to the C ABI declared
 in ``include/dgfp8.h`` and raises ``DgError`` on a non-zero status.  All
 arithmetic runs in the HIP kernels of ``libdgfp8.so``; there is no fallback:
-importing this package fails loudly when the library has not been built.
+importing this package fails loudly when the library has not been built.  The
+marshalling of the mixture-of-experts and int8 operators is compiled
+(``_native.so``).
 
 Tensor conventions (torch): E4M3 operands are ``torch.float8_e4m3fn`` (or
 ``torch.uint8`` holding the codes), scales ``torch.float32`` with any
@@ -27,6 +29,10 @@ LIB_PATH = os.path.join(_HERE, "libdgfp8.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python moe_fp8_gemm_amd/build.py`")
+
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
+if not os.path.exists(NATIVE_PATH):
+    raise ImportError(f"{NATIVE_PATH} is missing: build it with `python moe_fp8_gemm_amd/build.py`")
 
 lib = ctypes.CDLL(LIB_PATH)
 
@@ -451,6 +457,10 @@ def set_dense_plan(instance: int, splits: int = 1) -> None:
 # named beside it have no counterpart here.
 set_num_sms = set_num_cus
 get_num_sms = get_num_cus
+
+from . import _native  # noqa: E402
+
+_native.connect(DgError, _auto_workspace)
 
 from .int8 import (int8_gemm_nt, m_grouped_int8_gemm_nt_contiguous, m_grouped_int8_gemm_nt_masked,  # noqa: E402
                    per_token_cast_int8)

@@ -1,4 +1,4 @@
-"""Build libdgfp8.so in-tree with hipcc for gfx950.
+"""Build libdgfp8.so in-tree with hipcc for gfx950, and _native.so, the torch binding's marshalling, with g++.
 
     python moe_fp8_gemm_amd/build.py [-v]
 
@@ -22,11 +22,13 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdgfp8.so")
+NATIVE_PATH = os.path.join(HERE, "_native.so")
 SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "gemm_int8.hip", "gemm_int8_rows.hip", "cast_fp8.hip",
            "scratch.hip", "moe_route.hip", "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip"]
 ARCH = "gfx950"
@@ -118,10 +120,44 @@ def _compile(src: str, verbose: bool):
     return obj, parse_resource_remarks(r.stderr or "")
 
 
+def _compile_binding(verbose: bool) -> str:
+    """Object of the marshalling module (host code on torch's and Python's headers)."""
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{d}" for d in includes] +
+           [os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    """_native.so finds libdgfp8.so beside itself and torch's libraries in the process, which has imported torch."""
+    from torch.utils import cpp_extension
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = (["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libdgfp8.so", "-Wl,-rpath,$ORIGIN"] +
+           [f"-L{d}" for d in cpp_extension.library_paths()] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"])
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _native.so failed:\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding = binding.result()
     objs = [o for o, _ in results]
     kernels = [k for _, ks in results for k in ks]
     table = resource_table(kernels)
@@ -142,6 +178,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding, verbose)
     return LIB_PATH
 
 
