@@ -439,9 +439,9 @@ def cpu_baseline():
 
 
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_dense_gemm.txt")
-# The GEMM kernels' source: the kernel file and the two headers it includes.
+# The GEMM kernels' source: the kernel file and the headers it includes.
 GEMM_SOURCES = [os.path.join(ROOT, "moe_fp8_gemm_amd", "csrc", f)
-                for f in ("gemm_fp8.hip", "dgfp8_device.h", "dgfp8_internal.h")]
+                for f in ("gemm_fp8.hip", "gemm_core.h", "dgfp8_device.h", "dgfp8_internal.h")]
 
 
 def gemm_source_sha256():
