@@ -603,7 +603,14 @@ DG_EXPORT dg_status dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_ws(
 
 namespace {
 
-// Launch of a checked masked problem.
+// Launch of a checked masked problem on one instance.
+dg_status run_masked_on(GemmInstance inst, const GemmParams& p, void* stream) {
+  const InstanceInfo info = instance_info(inst);
+  const int64_t bound = (int64_t)p.num_groups * ceil_div(p.m, info.bm) * ceil_div(p.n, info.bn);
+  return launch(inst, kMasked, p, bound, static_cast<hipStream_t>(stream));
+}
+
+// Launch of a checked masked FP8 problem.
 dg_status run_masked(const GemmParams& p, int64_t expected_m, void* stream) {
   // Each group's B is streamed once per M tile: a 256-row tile covers groups
   // of up to 256 rows in one pass.  When the caller expects few rows per group
@@ -613,9 +620,42 @@ dg_status run_masked(const GemmParams& p, int64_t expected_m, void* stream) {
   // so the results are the same bits whichever instance runs.
   const GemmInstance inst = (expected_m > 0 && expected_m <= 64) ? kInstDecode
                             : (p.m > 128 ? kInstHuge : kInstLarge);
-  const InstanceInfo info = instance_info(inst);
-  const int64_t bound = (int64_t)p.num_groups * ceil_div(p.m, info.bm) * ceil_div(p.n, info.bn);
-  return launch(inst, kMasked, p, bound, static_cast<hipStream_t>(stream));
+  return run_masked_on(inst, p, stream);
+}
+
+// The masked int8 product's kernel.  Its sums are exact, so every choice gives the same
+// bits and expected_m (unknown: max_m) decides on speed alone.  While there is less than
+// a tile for every CU, a tile's own latency counts: the K loop moves 0.45 us a block on
+// 64x64 tiles, 0.7 on 128x128, 0.9 on 64x256, so the smallest tiles that still fit the
+// device at once win; with very few rows the row kernel does (us, counts drawn from
+// 0 .. 2 expected_m):
+//    G x N x K       expected  rows  64x64  128x128  64x256
+//    2x880x6176          4      6.9    27      45      64
+//    8x1024x4096        12     16.5    15.2    22      29
+//    2x4096x7168        12     18.7    23      34      48
+//    8x2048x4096         4     18.9    17.5    27      32
+//    4x4096x7168        40     89      32      45      53
+//    6x4096x2048         4     16.1    16.1    15.2    18.4
+//    12x4096x7168        4     70      73      82      66
+//    16x4096x7168        4     89      93      84      75
+// Past that it is how often B is read: 64x256 tiles while nearly all groups fit 64 rows,
+// then 128 rows (16x4096x7168 expected 40: 120 us on 64x256, 90 on 128x256) or, above
+// 64 with room for them, 256 (expected 90: 155, 135, 122 on 256x256).
+constexpr int64_t kInt8MaskedRows = 16;
+dg_status run_masked_int8(const GemmParams& p, int64_t expected_m, void* stream) {
+  const int64_t rows = expected_m > 0 && expected_m < p.m ? expected_m : p.m, cus = device_cus();
+  if (rows <= kInt8MaskedRows && p.num_groups * ceil_div(p.n, 16) <= 2 * cus)
+    return launch_gemm_int8_rows_masked(p, static_cast<hipStream_t>(stream)) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+  const auto fits = [&](GemmInstance inst) {
+    const InstanceInfo info = instance_info(inst);
+    return p.num_groups * ceil_div(rows, info.bm) * ceil_div(p.n, info.bn) <= cus;
+  };
+  const GemmInstance inst = fits(kInstSkinny64)           ? kInstSkinny64
+                            : fits(kInstMid)              ? kInstMid
+                            : rows <= 32                  ? kInstDecode
+                            : rows <= 64 || p.m <= 128    ? kInstLarge
+                                                          : kInstHuge;
+  return run_masked_on(inst, p, stream);
 }
 
 dg_status grouped_masked(const void* a, int64_t lda, int64_t a_group_stride, const void* sfa, int64_t sfa_sm,
@@ -791,7 +831,7 @@ DG_EXPORT dg_status dg_m_grouped_int8_gemm_nt_masked(
   p.b_gs = b_group_stride;
   p.sfb_gs = sfb_group_stride;
   p.masked_m = masked_m;
-  return run_masked(p, expected_m, stream);
+  return run_masked_int8(p, expected_m, stream);
 }
 
 namespace {

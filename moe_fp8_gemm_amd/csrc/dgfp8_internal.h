@@ -88,6 +88,8 @@ hipError_t launch_gemm_int8(GemmInstance inst, Variant v, const GemmParams& p, i
 // int8 dense GEMM of at most kInt8Rows rows.
 constexpr int64_t kInt8Rows = 8;
 hipError_t launch_gemm_int8_rows(const GemmParams& p, hipStream_t stream);
+// int8 masked GEMM for few rows a group (any number is right).
+hipError_t launch_gemm_int8_rows_masked(const GemmParams& p, hipStream_t stream);
 
 struct CastParams {
   const void* x;

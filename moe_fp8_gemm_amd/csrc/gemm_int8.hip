@@ -8,7 +8,7 @@ hipError_t launch_gemm_int8(GemmInstance inst, Variant v, const GemmParams& p, i
   switch (inst) {
     case kInstHuge: return launch_variant<Int8Cfg<CfgHuge>, (1 << kDense) | (1 << kMasked) | (1 << kContiguous)>(v, p, grid, stream);
     case kInstSkinny128: return launch_variant<Int8Cfg<CfgSkinny128>, kDenseAndSplit>(v, p, grid, stream);
-    case kInstSkinny64: return launch_variant<Int8Cfg<CfgSkinny64>, kDenseAndSplit>(v, p, grid, stream);
+    case kInstSkinny64: return launch_variant<Int8Cfg<CfgSkinny64>, kDenseAndSplit | (1 << kMasked)>(v, p, grid, stream);
     case kInstLarge: return launch_variant<Int8Cfg<CfgLarge>, kAll>(v, p, grid, stream);
     case kInstMid: return launch_variant<Int8Cfg<CfgMid>, kAll>(v, p, grid, stream);
     case kInstDecode: return launch_variant<Int8Cfg<CfgDecode>, (1 << kMasked)>(v, p, grid, stream);

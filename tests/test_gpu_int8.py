@@ -228,6 +228,33 @@ def test_masked(g, max_m, n, k, expected_m, dtype):
     assert same(d, want)
 
 
+@pytest.mark.parametrize("cus", [0, 3, 20])
+@pytest.mark.parametrize("expected_m", [0, 1, 16, 17, 40, 90])
+def test_masked_plans_agree(expected_m, cus):
+    """The hint and the grid width pick the kernel (few rows, 64 to 256 row tiles), never a bit of the result; groups
+    hold none to all of the rows whatever the hint says, and K ends inside a block."""
+    g, max_m, n, k = 5, 150, 328, 1552
+    rng = np.random.default_rng(7)
+    masked_m = np.array([0, 1, 17, 150, 65], np.int32)
+    qa = rng.integers(-128, 128, (g, max_m, k)).astype(np.int8)
+    sa = (rng.random((g, max_m)) * 0.02 + 1e-4).astype(np.float32)
+    qb = rng.integers(-128, 128, (g, n, k)).astype(np.int8)
+    sb = (rng.random((g, n)) * 0.02 + 1e-4).astype(np.float32)
+    dtype = torch.bfloat16
+    want = torch.full((g, max_m, n), FILL, dtype=dtype)
+    for i, c in enumerate(masked_m):
+        if c:
+            want[i, :c] = expected(dtype, qa[i, :c], sa[i, :c], qb[i], sb[i])
+    d = torch.full((g, max_m, n), FILL, dtype=dtype, device=device())
+    try:
+        dg.set_num_cus(cus)
+        dg.m_grouped_int8_gemm_nt_masked((upload(qa), upload(sa)), (upload(qb), upload(sb)), d, upload(masked_m),
+                                         expected_m)
+    finally:
+        dg.set_num_cus(0)
+    assert same(d, want)
+
+
 def test_graph_replays():
     """Dense with a K split, contiguous and masked in one graph; eager calls on the same workspace between replays."""
     ops = operands(64, 512, 2064, seed=3)
