@@ -461,6 +461,28 @@ ContigDecision decide_contiguous(int64_t m_total, int64_t n, int64_t k, int num_
   return dec;
 }
 
+// int8 sums are exact, so its plan is free to follow speed alone; with a workspace and
+// few tiles, one launch splits K over the blocks that are no padding (us, against
+// one 128-row tile per block: 2x2704x2672, 2 blocks, 25 to 16; 2x4096x7168, 3 blocks, 40
+// to 28; 8x1480x4416, 10 blocks, 36 to 28; 4x1024x2048, 6 blocks, 13 and 13: the hand-over of
+// the partial tiles eats what a split of 16 K blocks gains; 3, 4 and 8 K blocks at least
+// per unit came within 5% but for 2 blocks, 16, 16 and 19, and 1 block, 23, 23 and 19).
+constexpr int kInt8MinKbPerSplit = 6;
+bool int8_contiguous_split(int64_t m_total, int64_t n, int64_t k) {
+  return g_contig_plan == 0 && m_total / kContiguousAlignment * ceil_div(n, 128) * 2 <= hw_cus() && k / 128 >= 20;
+}
+ContigSplit int8_contiguous_split_plan(int64_t m_total, int64_t n, int64_t k) {
+  ContigSplit cs = contig_split(kInstMid, m_total / kContiguousAlignment, n, k, 1, hw_cus());
+  cs.cap = (int)std::min<int64_t>(k / 128 / kInt8MinKbPerSplit, 64);
+  return cs;
+}
+// Pairs of blocks pay where groups have many: 8x4096x7168 and 4x4096x4096 at 8 and 16 blocks
+// a group 2% less, 16x4096x2048 at 2.4 blocks 80 us against 55, 32x2048x7168 at 4
+// blocks 296 against 240 without.
+bool int8_contiguous_pairs(int64_t m_total, int num_groups) {
+  return g_contig_plan != 0 || m_total / kContiguousAlignment >= 8 * (int64_t)num_groups;
+}
+
 // Launches of a checked contiguous problem.
 dg_status run_contiguous(const GemmParams& p, void* ws, size_t ws_bytes, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -479,7 +501,21 @@ dg_status run_contiguous(const GemmParams& p, void* ws, size_t ws_bytes, void* s
   // the results (which the split's summation order affects) do not depend on
   // the override.
   const int64_t nblocks = m_total / kContiguousAlignment;
-  const ContigDecision dec = decide_contiguous(m_total, n, k, num_groups, ws != nullptr ? ws_bytes : 0);
+  if (p.int8 && ws != nullptr && int8_contiguous_split(m_total, n, k)) {
+    const ContigSplit cs = int8_contiguous_split_plan(m_total, n, k);
+    if ((int64_t)ws_bytes >= cs.ws_bytes) {
+      GemmParams ps = p;
+      ps.contig_mode = 3;
+      ps.counters = static_cast<int*>(ws);
+      ps.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
+      ps.splits = cs.cap;
+      ps.kb_per_split = (int)(k / 128);
+      ps.contig_split_units = cs.units;
+      return launch(kInstMid, kContiguousSplitK, ps, cs.units, s);
+    }
+  }
+  ContigDecision dec = decide_contiguous(m_total, n, k, num_groups, ws != nullptr ? ws_bytes : 0);
+  if (p.int8 && !int8_contiguous_pairs(m_total, num_groups)) dec.paired = false;
   if (dec.paired) {
     const InstanceInfo hi = instance_info(kInstHuge);
     GemmParams pp = p;
@@ -780,6 +816,11 @@ DG_EXPORT dg_status dg_int8_gemm_nt(const void* a, int64_t lda, const float* sfa
 
 DG_EXPORT size_t dg_m_grouped_int8_gemm_nt_contiguous_workspace_size(int64_t m_total, int64_t n, int64_t k,
                                                                      int num_groups) {
+  if (m_total <= 0 || n <= 0 || k <= 0 || num_groups < 1 || m_total % kContiguousAlignment != 0 ||
+      !dims_ok(m_total, n, k))
+    return 0;
+  if (int8_contiguous_split(m_total, n, k)) return (size_t)int8_contiguous_split_plan(m_total, n, k).ws_bytes;
+  if (!int8_contiguous_pairs(m_total, num_groups)) return 0;
   return dg_m_grouped_fp8_gemm_nt_contiguous_workspace_size(m_total, n, k / 128 * 128, num_groups);
 }
 

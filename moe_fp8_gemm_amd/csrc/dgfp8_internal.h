@@ -46,7 +46,8 @@ struct GemmParams {
   int sf_packed;
   // contiguous only: 0 = a tile per BM-row block; 1 = 256-row tiles on pairs of
   // consecutive blocks of one group; 2 = 128-row tiles on the blocks no pair
-  // covers (tile lists built on the device from m_indices)
+  // covers (tile lists built on the device from m_indices); 3 (int8) = 128-row
+  // tiles on every block that is no padding
   int contig_mode;
   // kContiguousSplitK only: the K split s is the largest with
   // (listed blocks) x (N tiles) x s <= contig_split_units, at most `splits`

@@ -577,6 +577,20 @@ __device__ void contig_tile_list(const GemmParams& p, int lane, DG_LAS int16_t* 
   if (lane == 63) *count = run;
 }
 
+// Mode 3 (int8): lists every block that is no padding, 64 blocks a round.
+__device__ void contig_block_list(const GemmParams& p, int lane, DG_LAS int16_t* list, DG_LAS int* count) {
+  const int nb = (int)(p.m / kKBlock);
+  int n = 0;
+  for (int b0 = 0; b0 < nb; b0 += 64) {
+    const int b = b0 + lane;
+    const bool listed = b < nb && p.m_indices[(int64_t)b * kKBlock] >= 0;
+    const uint64_t mask = __builtin_amdgcn_ballot_w64(listed);
+    if (listed) list[n + __builtin_popcountll(mask & ((1ull << lane) - 1))] = (int16_t)b;
+    n += __builtin_popcountll(mask);
+  }
+  if (lane == 0) *count = n;
+}
+
 template <class C, int V>
 __global__ void __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(C::kWaves * C::kOcc / 4, C::kWaves * C::kOcc / 4)))
@@ -641,7 +655,12 @@ gemm_kernel(GemmParams p) {
   __shared__ int contig_count;
   if constexpr (kContig) {
     if (p.contig_mode != 0) {
-      if (wave == 0) contig_tile_list(p, lane, (DG_LAS int16_t*)contig_list, (DG_LAS int*)&contig_count);
+      if (wave == 0) {
+        if (C::kInt8 && p.contig_mode == 3)
+          contig_block_list(p, lane, (DG_LAS int16_t*)contig_list, (DG_LAS int*)&contig_count);
+        else
+          contig_tile_list(p, lane, (DG_LAS int16_t*)contig_list, (DG_LAS int*)&contig_count);
+      }
       __syncthreads();
       tiles_m = contig_count;
       if constexpr (V == kContiguousSplitK) {

@@ -204,6 +204,30 @@ def test_contiguous(counts, n, k, dtype):
         dg.set_contiguous_plan(0)
 
 
+@pytest.mark.parametrize("counts,pad,n,k", [([1], 0, 8, 2560), ([0, 0], 2, 72, 2576), ([5, 0, 200], 1, 200, 2688 + 48),
+                                            ([130, 127, 1, 90], 3, 264, 7168), ([129], 70, 128, 4096 + 16)])
+def test_contiguous_split(counts, pad, n, k):
+    """Few blocks and a long K: one launch that splits K over the blocks that are no padding; the workspace serves
+    call after call, the second on other data."""
+    for seed in (1, 2):
+        m_idx, qa, sa, qb, sb = contiguous_case(counts, n, k, seed)
+        m_idx = np.concatenate([np.full(128 * (pad // 2), -1), m_idx, np.full(128 * (pad - pad // 2), -1)]).astype(np.int32)
+        lo = 128 * (pad // 2)
+        qa = np.concatenate([np.zeros((lo, k), np.int8), qa, np.zeros((m_idx.size - lo - len(qa), k), np.int8)])
+        sa = np.concatenate([np.full(lo, np.nan), sa, np.full(m_idx.size - lo - len(sa), np.nan)]).astype(np.float32)
+        want = torch.full((m_idx.size, n), FILL, dtype=torch.bfloat16)
+        for g in range(len(counts)):
+            if counts[g]:
+                rows = torch.from_numpy(m_idx == g)
+                want[rows] = expected(torch.bfloat16, qa[m_idx == g], sa[m_idx == g], qb[g], sb[g])
+        for ws in ("auto", None):
+            d = torch.full((m_idx.size, n), FILL, dtype=torch.bfloat16, device=device())
+            if m_idx.size:
+                dg.m_grouped_int8_gemm_nt_contiguous((upload(qa), upload(sa)), (upload(qb), upload(sb)), d,
+                                                     upload(m_idx), workspace=ws)
+            assert same(d, want), ws
+
+
 @pytest.mark.parametrize("dtype", OUT)
 @pytest.mark.parametrize("g,max_m,n,k", [(1, 1, 8, 16), (5, 64, 100, 208), (3, 200, 264, 656), (16, 256, 72, 1040)])
 @pytest.mark.parametrize("expected_m", [1, 100])
