@@ -24,17 +24,20 @@
 // Layout.  A token belongs to kLanes lanes of one wave, each lane holding a run of
 // kVals consecutive experts in registers: the run makes wide loads, and lower
 // lanes hold lower expert numbers.  16 lanes serve four tokens with each
-// instruction; a whole wave takes the sizes that 16 lanes do not hold (over 256
-// experts, or over 16 slots).
+// instruction; a whole wave takes few tokens, where its shorter chain of instructions
+// counts, and the sizes that 16 lanes do not hold (over 256 experts, or over 16 slots).
 //
 // Choice.  Instead of topk rounds of "find the maximum and take it out", a bound
-// that at least topk keys reach is taken from the lanes' maxima; the few keys that
+// that at least topk keys reach is taken from 16 maxima; the few keys that
 // reach it (about 11 of 256 for the top 8) are packed one to a lane, in
 // order of expert number, and each lane counts how many come before its own: its slot.
 // Where more than kLanes keys reach the bound it is raised by halving; where that
-// does not help (equal keys) the rounds run after all.  Measured on 32768 x 256
-// bf16 logits, top 8: 18.1 us with rounds alone, 10.4 us so; with sigmoid
-// scores, a bias and 4 of 8 groups 24.6 us; one token 4.0 us.
+// does not help (equal keys) the rounds run after all.  Every step is written for all
+// values at once and without branches: a lone wave's time is its chain of
+// instructions at 7 to 8 cycles each.  Measured on 32768 x 256 bf16 logits, top 8: 18.1 us
+// with rounds alone, 9.2 us so (16.8 MB; the vector instructions bound it); with sigmoid
+// scores, a bias and 4 of 8 groups of fp32 logits 18.5 us; one token 3.3 and 4.6 us, an
+// empty launch 2.3.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -48,20 +51,26 @@ constexpr int kNone = INT32_MIN;   // rank of an expert that cannot be chosen
 
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);   // every lane has a source
 }
 constexpr int kRowRor = 0x120;     // rotate right within a row of 16 lanes
+constexpr int kRowLast = 0x15F;    // the value of a row's last lane
 
+// Over the lanes of the same place in a wave's four rows of 16.
+template <class Op>
+__device__ __forceinline__ int join_rows(int v, Op op) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);   // even rows' values, odd rows' values
+  v = op((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);   // lower half's, upper half's
+  return op((int)b[0], (int)b[1]);
+}
 template <int kLanes, class Op>
 __device__ __forceinline__ int reduce(int v, Op op) {
   v = op(v, dpp<kRowRor + 8>(v));
   v = op(v, dpp<kRowRor + 4>(v));
   v = op(v, dpp<kRowRor + 2>(v));
   v = op(v, dpp<kRowRor + 1>(v));
-  if constexpr (kLanes == 64) {
-    v = op(v, __shfl_xor(v, 16, 64));
-    v = op(v, __shfl_xor(v, 32, 64));
-  }
+  if constexpr (kLanes == 64) v = join_rows(v, op);
   return v;
 }
 template <int kLanes>
@@ -127,30 +136,41 @@ __device__ __forceinline__ float sigmoid_for_rank(float x) {
   return __builtin_amdgcn_rcpf(1.0f + exp_for_rank(-x));
 }
 
-// A lane's run of logits; experts past the last are -inf.  `wide`: rows start at
-// 16-byte boundaries, so whole 16-byte pieces of a run load at once.
+// Values of a lane's run that load at once.
 template <class T, int kVals>
-__device__ __forceinline__ void load_run(const void* logits, int64_t row_off, int e0, int experts, bool wide,
-                                         float (&x)[kVals]) {
+constexpr int kPiece = 16 / sizeof(typename T::store) < kVals ? 16 / sizeof(typename T::store) : kVals;   // values
+// A lane's kVals logits, -inf past the last expert: piece c of kPer values (8 or 16
+// bytes) begins at expert e0 + c * step.  `wide`: rows start at 16-byte boundaries.  Where
+// the experts fill whole pieces they load at once.  What lies past the end loads the
+// row's first instead, so that no lane goes another way and all loads are in flight
+// together.
+template <class T, int kVals, int kPer>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t row_off, int e0, int step, int experts,
+                                            bool wide, float (&x)[kVals]) {
   typedef typename T::store S;
-  const S* src = (const S*)logits + row_off + e0;
-  constexpr int kPer = 16 / sizeof(S) < kVals ? 16 / sizeof(S) : kVals;   // values of one wide load
+  const S* row = (const S*)logits + row_off;
+  if (wide && experts % kPer == 0) {
+    typedef uint32_t words __attribute__((ext_vector_type(kPer * sizeof(S) / 4)));
+    words v[kVals / kPer];
 #pragma unroll
-  for (int c = 0; c < kVals; c += kPer) {
-    if (kPer * sizeof(S) == 16 && wide && e0 + c + kPer <= experts) {
-      const u32x4 v = *(const u32x4*)(src + c);
+    for (int c = 0; c < kVals / kPer; ++c) v[c] = *(const words*)(row + (e0 + c * step < experts ? e0 + c * step : 0));
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if constexpr (sizeof(S) == 4) {
-          x[c + i] = __uint_as_float(v[i]);
-        } else {
-          x[c + i] = widen(T{}, (uint16_t)(v[i / 2] >> (16 * (i & 1))));
-        }
+    for (int i = 0; i < kVals; ++i) {
+      const int c = i / kPer, o = i % kPer;
+      float f;
+      if constexpr (sizeof(S) == 4) {
+        f = __uint_as_float(v[c][o]);
+      } else {
+        f = widen(T{}, (uint16_t)(v[c][o / 2] >> (16 * (o & 1))));
       }
-    } else {
+      x[i] = e0 + c * step < experts ? f : -__builtin_inff();
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        x[c + i] = e0 + c + i < experts ? widen(T{}, src[c + i]) : -__builtin_inff();
+    for (int i = 0; i < kVals; ++i) {
+      const int e = e0 + i / kPer * step + i % kPer;
+      const float f = widen(T{}, row[e < experts ? e : 0]);
+      x[i] = e < experts ? f : -__builtin_inff();
     }
   }
 }
@@ -167,6 +187,11 @@ __device__ __forceinline__ int largest(const int (&v)[kVals]) {
 // groups of 32, 64, ... experts side by side meet different banks.
 __device__ __forceinline__ int key_slot(int e) { return e + (e >> 5); }
 
+// Words of a token's list of keys: expert numbers, ranks, logits, each with as many places
+// for what is not listed.
+template <int kLanes>
+constexpr int kFound = 2 * kLanes;
+
 // What a lane holds of the choice: the expert (-1: the slot stays empty), its logit, and
 // its slot (topk or more: nothing).
 struct Chosen {
@@ -177,7 +202,7 @@ struct Chosen {
 // The choice in topk rounds; any number of equal keys.
 template <int kLanes, int kVals>
 __device__ __forceinline__ Chosen choose_by_rounds(int (&rank)[kVals], const float (&x)[kVals], int lane, int e0,
-                                                   int topk, int* experts, float* logits) {
+                                                   int topk, int* experts, int* logits) {
   int mine = largest(rank);
   for (int j = 0; j < topk; ++j) {
     const int best = max_lanes<kLanes>(mine);
@@ -192,7 +217,7 @@ __device__ __forceinline__ Chosen choose_by_rounds(int (&rank)[kVals], const flo
       }
     if (winner) {
       experts[j] = best <= kRankLow ? -1 : e0 + at;
-      logits[j] = logit;
+      logits[j] = __float_as_int(logit);
     }
     at = winner ? at : -1;
 #pragma unroll
@@ -201,33 +226,30 @@ __device__ __forceinline__ Chosen choose_by_rounds(int (&rank)[kVals], const flo
   }
   wave_sync();
   Chosen c{-1, kLanes, 0.0f};
-  if (lane < topk) c = {experts[lane], lane, logits[lane]};
+  if (lane < topk) c = {experts[lane], lane, __int_as_float(logits[lane])};
   return c;
 }
 
 template <int kLanes, int kVals>
 __device__ __forceinline__ Chosen choose(int (&rank)[kVals], const float (&x)[kVals], int lane, int e0, int topk,
-                                         int* experts, float* logits, int* ranks) {
-  // ---- a bound that at least topk keys reach: the topk-th largest of 16 lane
-  // maxima, or of a wave's lanes in as many groups as slots the least group maximum
+                                         int* found) {
+  // ---- a bound that at least topk keys reach: the topk-th largest of 16 maxima (of a
+  // lane each, or of four lanes of a wave); past 16 slots the least maximum of the wave's
+  // lanes, or pairs of them
   const int mine = largest(rank);
   int bound;
-  if constexpr (kLanes == 16) {
+  if (kLanes == 16 || topk <= 16) {
+    const int m = kLanes == 16 ? mine : join_rows(mine, [](int a, int b) { return max(a, b); });
     int above = 0;
-    auto count = [&](int other) { above += other > mine ? 1 : 0; };
-    count(dpp<kRowRor + 1>(mine)); count(dpp<kRowRor + 2>(mine)); count(dpp<kRowRor + 3>(mine));
-    count(dpp<kRowRor + 4>(mine)); count(dpp<kRowRor + 5>(mine)); count(dpp<kRowRor + 6>(mine));
-    count(dpp<kRowRor + 7>(mine)); count(dpp<kRowRor + 8>(mine)); count(dpp<kRowRor + 9>(mine));
-    count(dpp<kRowRor + 10>(mine)); count(dpp<kRowRor + 11>(mine)); count(dpp<kRowRor + 12>(mine));
-    count(dpp<kRowRor + 13>(mine)); count(dpp<kRowRor + 14>(mine)); count(dpp<kRowRor + 15>(mine));
-    bound = min_lanes<kLanes>(above < topk ? mine : INT32_MAX);
+    auto count = [&](int other) { above += other > m ? 1 : 0; };
+    count(dpp<kRowRor + 1>(m)); count(dpp<kRowRor + 2>(m)); count(dpp<kRowRor + 3>(m));
+    count(dpp<kRowRor + 4>(m)); count(dpp<kRowRor + 5>(m)); count(dpp<kRowRor + 6>(m));
+    count(dpp<kRowRor + 7>(m)); count(dpp<kRowRor + 8>(m)); count(dpp<kRowRor + 9>(m));
+    count(dpp<kRowRor + 10>(m)); count(dpp<kRowRor + 11>(m)); count(dpp<kRowRor + 12>(m));
+    count(dpp<kRowRor + 13>(m)); count(dpp<kRowRor + 14>(m)); count(dpp<kRowRor + 15>(m));
+    bound = min_lanes<16>(above < topk ? m : INT32_MAX);   // every row has the same
   } else {
-    int g = mine;   // maximum of this lane's group of 64 / 2^n >= topk lanes
-    if (topk <= 32) g = max(g, swap_lanes<1>(g));
-    if (topk <= 16) g = max(g, swap_lanes<2>(g));
-    if (topk <= 8) g = max(g, swap_lanes<4>(g));
-    if (topk <= 4) g = max(g, swap_lanes<8>(g));
-    bound = min_lanes<kLanes>(g);
+    bound = min_lanes<kLanes>(topk <= 32 ? max(mine, swap_lanes<1>(mine)) : mine);
   }
   bound = max(bound, kRankLow + 1);
 
@@ -238,44 +260,53 @@ __device__ __forceinline__ Chosen choose(int (&rank)[kVals], const float (&x)[kV
     for (int i = 0; i < kVals; ++i) n += rank[i] >= b ? 1 : 0;
     return n;
   };
+  auto sum = [&](int before_and_own) {
+    return kLanes == 16 ? dpp<kRowLast>(before_and_own) : __builtin_amdgcn_readlane(before_and_own, 63);
+  };
   int n = reach(bound);
   int at = sum_before<kLanes>(n);
-  int total = max_lanes<kLanes>(at + n);
-  // more than fit: halve the way to the largest key while at least topk reach the middle
-  int over = max_lanes<kLanes>(mine);              // fewer than topk keys are above it, or none fits
-  for (int pass = 0; pass < 8 && __builtin_amdgcn_ballot_w64(total > kLanes) != 0; ++pass) {
-    const int mid = bound + (int)(((uint32_t)over - (uint32_t)bound + 1) >> 1);
-    const int nm = reach(mid), am = sum_before<kLanes>(nm), tm = max_lanes<kLanes>(am + nm);
-    if (total > kLanes) {
-      if (tm >= topk) {
-        bound = mid;
-        n = nm;
-        at = am;
-        total = tm;
-      } else {
-        over = mid - 1;
+  int total = sum(at + n);
+  if (__builtin_amdgcn_ballot_w64(total > kLanes) != 0) {
+    // more than fit: halve the way to the largest key while at least topk reach the middle
+    int over = max_lanes<kLanes>(mine);              // fewer than topk keys are above it, or none fits
+    for (int pass = 0; pass < 8 && __builtin_amdgcn_ballot_w64(total > kLanes) != 0; ++pass) {
+      const int mid = bound + (int)(((uint32_t)over - (uint32_t)bound + 1) >> 1);
+      const int nm = reach(mid), am = sum_before<kLanes>(nm), tm = sum(am + nm);
+      if (total > kLanes) {
+        if (tm >= topk) {
+          bound = mid;
+          n = nm;
+          at = am;
+          total = tm;
+        } else {
+          over = mid - 1;
+        }
       }
     }
+    if (__builtin_amdgcn_ballot_w64(total > kLanes) != 0)   // any token of the wave
+      return choose_by_rounds<kLanes, kVals>(rank, x, lane, e0, topk, found, found + 2 * kFound<kLanes>);
   }
-  if (__builtin_amdgcn_ballot_w64(total > kLanes) != 0)   // any token of the wave
-    return choose_by_rounds<kLanes, kVals>(rank, x, lane, e0, topk, experts, logits);
-  experts[lane] = -1;
-  ranks[lane] = kNone;
-  wave_sync();
+  // every lane writes every value, those below the bound to a place of its own that
+  // nobody reads: no branches, which would cost more than the writes
+  int* const ranks = found + kFound<kLanes>;
+  int* const logits = ranks + kFound<kLanes>;
 #pragma unroll
-  for (int i = 0; i < kVals; ++i)
-    if (rank[i] >= bound) {
-      experts[at] = e0 + i;
-      ranks[at] = rank[i];
-      logits[at] = x[i];
-      ++at;
-    }
+  for (int i = 0; i < kVals; ++i) {
+    const bool in = rank[i] >= bound;
+    const int to = in ? at : kLanes + lane;
+    found[to] = e0 + i;
+    ranks[to] = rank[i];
+    logits[to] = __float_as_int(x[i]);
+    at += in ? 1 : 0;
+  }
   wave_sync();
 
   // ---- each lane counts the keys before its own: larger, or equal in a lower lane
-  const int key = ranks[lane];
+  const bool listed = lane < total;
+  const int key = listed ? ranks[lane] : kNone;
   int before = 0;
-  if constexpr (kLanes == 16) {
+  const int keys = kLanes == 64 ? __builtin_amdgcn_readfirstlane(total) : 0;
+  if (kLanes == 16 || keys <= 16) {   // a row of lanes holds them
     auto count = [&](int other, bool lower) { before += other > key || (other == key && lower) ? 1 : 0; };
     // row_ror r hands lane i the key of lane (i + 16 - r) % 16, which is lower where i >= r
     count(dpp<kRowRor + 1>(key), lane >= 1); count(dpp<kRowRor + 2>(key), lane >= 2);
@@ -287,14 +318,13 @@ __device__ __forceinline__ Chosen choose(int (&rank)[kVals], const float (&x)[kV
     count(dpp<kRowRor + 13>(key), lane >= 13); count(dpp<kRowRor + 14>(key), lane >= 14);
     count(dpp<kRowRor + 15>(key), lane >= 15);
   } else {
-    const int keys = __builtin_amdgcn_readfirstlane(total);
     for (int j = 0; j < keys; ++j) {
       const int other = __builtin_amdgcn_readlane(key, j);
       before += other > key || (other == key && j < lane) ? 1 : 0;
     }
   }
   // the lanes without a key stand behind all others, in order: they are the empty slots
-  return {experts[lane], lane < total ? before : lane, logits[lane]};
+  return {listed ? found[lane] : -1, listed ? before : lane, __int_as_float(logits[lane])};
 }
 
 template <class T, int kLanes, int kVals, bool kGroups>
@@ -303,8 +333,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p) {
   constexpr int kKeys = kLanes * kVals + kLanes * kVals / 32;
   __shared__ int keys[kGroups ? kTokens * kKeys : 1];
   __shared__ __attribute__((aligned(16))) float group_score[kGroups ? kTokens * kMaxExpertGroups : 1];
-  __shared__ int experts[kTokens * kLanes], ranks[kTokens * kLanes];
-  __shared__ float logits[kTokens * kLanes];
+  __shared__ int found[kTokens * 3 * kFound<kLanes>];
   const int lane = threadIdx.x % kLanes;
   const int slot = threadIdx.x / kLanes;
   const int64_t token = (int64_t)blockIdx.x * kTokens + slot;
@@ -314,9 +343,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p) {
   const bool wide = ((uintptr_t)p.logits & 15) == 0 && (p.ld * sizeof(typename T::store)) % 16 == 0;
 
   float x[kVals];
-  load_run<T, kVals>(p.logits, row, e0, p.experts, wide, x);
+  load_logits<T, kVals, kPiece<T, kVals>>(p.logits, row, e0, kPiece<T, kVals>, p.experts, wide, x);
   float bias[kVals];
-  if (p.bias) load_run<F32, kVals>(p.bias, 0, e0, p.experts, ((uintptr_t)p.bias & 15) == 0, bias);
+  if (p.bias)
+    load_logits<F32, kVals, 4>(p.bias, 0, e0, 4, p.experts, ((uintptr_t)p.bias & 15) == 0, bias);
 
   // ---- logits without a score (NaN; +inf under softmax): taken out, and the
   // token's weights become NaN.  One look at the extremes of the ranks tells
@@ -358,17 +388,36 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p) {
   // ---- keys: with a bias, or for the groups' sums, scores take the logits' place
   int group_rank[kGroups ? kVals : 1];   // what the groups go by
   if (need_scores) {
-    const float inv = 1.0f / total;
+    // one decision at a time for all values, so that their chains overlap
+    float key[kVals];
+    if (softmax) {
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) key[i] = exp_for_rank(x[i] - top) * inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) key[i] = sigmoid_for_rank(x[i]);
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) key[i] += bias[i];
+    }
+    bool lost = false;   // a NaN key of an expert with a score (from the bias)
+    int key_rank[kVals];
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
-      float key = softmax ? exp_for_rank(x[i] - top) * inv : sigmoid_for_rank(x[i]);
-      if (p.bias) key += bias[i];
-      const bool in = x[i] != -__builtin_inff();
-      if (p.bias) {
-        nan |= in && key != key;
-        rank[i] = in && key == key ? rank_of(key) : kRankLow;
-      }
-      if constexpr (kGroups) group_rank[i] = in && key == key ? rank_of(key) : kRankLow;
+      const bool in = x[i] != -__builtin_inff(), number = key[i] == key[i];
+      lost |= in && !number;
+      key_rank[i] = in && number ? rank_of(key[i]) : kRankLow;
+    }
+    if constexpr (kGroups) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) group_rank[i] = key_rank[i];
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) rank[i] = key_rank[i];
+      nan |= lost;
     }
     if (p.bias) nan = token_ballot<kLanes>(nan) != 0;
   }
@@ -459,8 +508,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p) {
     }
   }
 
-  const Chosen c = choose<kLanes, kVals>(rank, x, lane, e0, p.topk, experts + slot * kLanes, logits + slot * kLanes,
-                                         ranks + slot * kLanes);
+  const Chosen c = choose<kLanes, kVals>(rank, x, lane, e0, p.topk, found + slot * 3 * kFound<kLanes>);
   const bool filled = c.slot < p.topk && c.expert >= 0;
 
   // ---- weights.  Renormalised softmax weights are the softmax over the chosen logits.
@@ -494,19 +542,54 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
   const bool live = token < p.tokens;
   const int64_t t = live ? token : p.tokens - 1;
   const int64_t row = t * p.ld;
-  const int e0 = lane * kVals;
+  // pieces of 4 experts, kLanes apart: a token's lanes meet whole lines, and the sums'
+  // order is that of every type
+  constexpr int kPer = 4;
+  const int e0 = lane * kPer;
   const bool softmax = p.score == DG_ROUTE_SOFTMAX;
   const bool dense = softmax && !p.renormalize;   // every expert of the row has a gradient
 
+  // every load first: the row's logits, then this lane's slots and their logits
   float x[kVals];
-  float top = -__builtin_inff(), total = 1.0f;
   if (dense) {
     const bool wide = ((uintptr_t)p.logits & 15) == 0 && (p.ld * sizeof(S)) % 16 == 0;
-    load_run<T, kVals>(p.logits, row, e0, p.experts, wide, x);
-    float m = -__builtin_inff();
+    load_logits<T, kVals, kPer>(p.logits, row, e0, kLanes * kPer, p.experts, wide, x);
+  }
+  constexpr int kSlots = 64 / kLanes;   // of a lane: slots lane, lane + kLanes, ...
+  int chosen[kSlots];                   // -1: none
+  float logit[kSlots], g[kSlots];
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) m = fmaxf(m, x[i]);
+  for (int k = 0; k < kSlots; ++k) {
+    chosen[k] = -1;
+    logit[k] = g[k] = 0.0f;
+    if (k > 0 && k * kLanes >= p.topk) continue;
+    const int j = lane + k * kLanes, at = j < p.topk ? j : 0;
+    const int e = p.indices[t * p.ldi + at];
+    g[k] = p.scale * p.dweights[t * p.ldw + at];
+    chosen[k] = j < p.topk && e >= 0 && e < p.experts ? e : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k)
+    if (k == 0 || k * kLanes < p.topk) logit[k] = widen(T{}, ((const S*)p.logits)[row + (chosen[k] < 0 ? 0 : chosen[k])]);
+
+  float* mine = part + slot * kRow;
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) mine[e0 + i / kPer * kLanes * kPer + i % kPer] = 0.0f;
+
+  float top = -__builtin_inff(), total = 1.0f;
+  if (softmax) {   // over the row, or renormalised over the chosen
+    float m = -__builtin_inff();
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) m = fmaxf(m, x[i]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k)
+        if (chosen[k] >= 0) m = fmaxf(m, logit[k]);
+    }
     top = value_of(max_lanes<kLanes>(rank_of(m)));
+  }
+  if (dense) {
     total = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
@@ -515,78 +598,60 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
     }
     total = sum_lanes<kLanes>(total);
   }
-  float* mine = part + slot * kRow;
-#pragma unroll
-  for (int i = 0; i < kVals; ++i) mine[e0 + i] = 0.0f;
-
-  auto expert_of = [&](int j) -> int {
-    const int e = p.indices[t * p.ldi + j];
-    return e >= 0 && e < p.experts ? e : -1;
-  };
-  auto logit_of = [&](int e) -> float { return widen(T{}, ((const S*)p.logits)[row + e]); };
-  if (softmax && p.renormalize) {
-    float m = -__builtin_inff();
-    for (int j = lane; j < p.topk; j += kLanes) {
-      const int e = expert_of(j);
-      if (e >= 0) m = fmaxf(m, logit_of(e));
-    }
-    top = value_of(max_lanes<kLanes>(rank_of(m)));
-  }
-  auto score_of = [&](int e) -> float {
-    const float v = logit_of(e);
-    if (!softmax) return sigmoid(v);
-    const float ex = expf(v - top);
-    return dense ? ex / total : ex;
-  };
+  const float inv = 1.0f / total;
   float sum = 0.0f, dot = 0.0f;   // of the chosen scores, and of gradient times score
-  for (int j = lane; j < p.topk; j += kLanes) {
-    const int e = expert_of(j);
-    if (e < 0) continue;
-    const float s = score_of(e);
-    sum += s;
-    dot += p.scale * p.dweights[t * p.ldw + j] * s;
+  float score[kSlots];
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k) {
+    score[k] = 0.0f;
+    if (chosen[k] < 0) continue;
+    score[k] = softmax ? expf(logit[k] - top) * inv : sigmoid(logit[k]);
+    sum += score[k];
+    dot += g[k] * score[k];
   }
   if (p.renormalize || dense) {
     sum = sum_lanes<kLanes>(sum);
     dot = sum_lanes<kLanes>(dot);
   }
   wave_sync();
-  for (int j = lane; j < p.topk; j += kLanes) {
-    const int e = expert_of(j);
-    if (e < 0) continue;
-    const float s = score_of(e);
-    float ds = p.scale * p.dweights[t * p.ldw + j];
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k) {
+    if (chosen[k] < 0) continue;
+    float ds = g[k];
     if (p.renormalize) ds = sum == 0.0f ? 0.0f : (ds - dot / sum) / sum;
-    mine[e] = softmax ? ds * s : ds * s * (1.0f - s);
+    mine[chosen[k]] = softmax ? ds * score[k] : ds * score[k] * (1.0f - score[k]);
   }
   wave_sync();
   if (!live) return;
   float out[kVals];
 #pragma unroll
-  for (int i = 0; i < kVals; ++i) {
-    out[i] = mine[e0 + i];
-    if (dense && total > 0.0f) out[i] -= x[i] / total * dot;
+  for (int i = 0; i < kVals; ++i) out[i] = mine[e0 + i / kPer * kLanes * kPer + i % kPer];
+  if (dense && total > 0.0f) {
+    const float share = inv * dot;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) out[i] -= x[i] * share;
   }
-  S* dst = (S*)p.dlogits + t * p.ldd + e0;
+  S* dst = (S*)p.dlogits + t * p.ldd;
   const bool wide_out = ((uintptr_t)p.dlogits & 15) == 0 && (p.ldd * sizeof(S)) % 16 == 0;
-  constexpr int kPer = 16 / sizeof(S) < kVals ? 16 / sizeof(S) : kVals;
 #pragma unroll
-  for (int c = 0; c < kVals; c += kPer) {
-    if (kPer * sizeof(S) == 16 && wide_out && e0 + c + kPer <= p.experts) {
-      u32x4 v;
+  for (int c = 0; c < kVals / kPer; ++c) {
+    const int e = e0 + c * kLanes * kPer;
+    if (wide_out && e + kPer <= p.experts) {
+      typedef uint32_t words __attribute__((ext_vector_type(kPer * sizeof(S) / 4)));
+      words v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < (int)(kPer * sizeof(S) / 4); ++i) {
         if constexpr (sizeof(S) == 4) {
-          v[i] = __float_as_uint(out[c + i]);
+          v[i] = __float_as_uint(out[c * kPer + i]);
         } else {
-          v[i] = (uint32_t)narrow(T{}, out[c + 2 * i]) | ((uint32_t)narrow(T{}, out[c + 2 * i + 1]) << 16);
+          v[i] = (uint32_t)narrow(T{}, out[c * kPer + 2 * i]) | ((uint32_t)narrow(T{}, out[c * kPer + 2 * i + 1]) << 16);
         }
       }
-      *(u32x4*)(dst + c) = v;
+      *(words*)(dst + e) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (e0 + c + i < p.experts) dst[c + i] = narrow(T{}, out[c + i]);
+        if (e + i < p.experts) dst[e + i] = narrow(T{}, out[c * kPer + i]);
     }
   }
 }
@@ -609,20 +674,32 @@ hipError_t grad_launch(const RouteGradParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// 16 lanes for a token where they hold it, with the smallest run that covers the
-// experts; a wave otherwise.  (A wave per token is no faster on few tokens either: 1
-// token of 256 experts, top 8: 4.2 us to 4.0; with a bias and 8 groups 8.2 to 7.8.)
+// 16 lanes for a token where they hold it, with the smallest run that covers the experts,
+// when the calls' waves fill the device.  With few tokens each wave's own chain of
+// instructions is what takes time, and a whole wave per token has a quarter of them per
+// lane (us, a wave to 16 lanes; 256 experts, top 8, sigmoid, bias, 4 of 8 groups: 1 token 4.6 to
+// 6.1, 2048 tokens 6.4 to 7.0, 4096 tokens 8.4 to 7.1; bf16 logits alone: 3.3 to 3.7, 4.1 to
+// 4.6, 4.9 to 4.7).  Groups that are no whole runs of 16 experts leave few lanes with keys
+// and so a low bound; four experts a lane find a better one (160 experts in 8 groups,
+// top 6: 1024 tokens 5.8 to 9.5, 8192 tokens 10.5 to 11.3, 16384 tokens 16.8 to 16.0).
+constexpr int64_t kWaveTokens = 2048, kWaveTokensOddGroups = 8192;
 template <class T>
 hipError_t route_sized(const RouteParams& p, hipStream_t s) {
   if (p.experts > 256) return route_launch<T, 64, 16>(p, s);
-  if (p.topk > 16) return route_launch<T, 64, 4>(p, s);
+  const bool odd_groups = p.experts > 128 && p.groups > 1 && p.experts / p.groups % 16 != 0;
+  if (p.topk > 16 || (p.experts > 64 && p.tokens <= (odd_groups ? kWaveTokensOddGroups : kWaveTokens)))
+    return route_launch<T, 64, 4>(p, s);
   if (p.experts <= 64) return route_launch<T, 16, 4>(p, s);
   if (p.experts <= 128) return route_launch<T, 16, 8>(p, s);
   return route_launch<T, 16, 16>(p, s);
 }
+// As for the forward pass (us, a wave to 16 lanes; 160 fp32 experts, top 6, plain softmax: 1
+// token 2.9 to 3.8, 2048 tokens 3.7 to 4.3, 4096 tokens 4.5 to 4.6, 32768 tokens 17.0 to
+// 12.4; 256 bf16 experts, renormalised: 2.6 to 3.2, 3.3 to 3.6, 3.8 to 3.8, 12.4 to 7.6).
 template <class T>
 hipError_t grad_sized(const RouteGradParams& p, hipStream_t s) {
   if (p.experts <= 64) return grad_launch<T, 16, 4>(p, s);
+  if (p.experts <= 256 && p.tokens <= kWaveTokens) return grad_launch<T, 64, 4>(p, s);
   if (p.experts <= 128) return grad_launch<T, 16, 8>(p, s);
   if (p.experts <= 256) return grad_launch<T, 16, 16>(p, s);
   return grad_launch<T, 64, 16>(p, s);
