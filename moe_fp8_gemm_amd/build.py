@@ -143,7 +143,7 @@ def _link_binding(obj: str, verbose: bool) -> None:
     from torch.utils import cpp_extension
     tmp = NATIVE_PATH + ".tmp"
     cmd = (["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libdgfp8.so", "-Wl,-rpath,$ORIGIN"] +
-           [f"-L{d}" for d in cpp_extension.library_paths()] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"])
+           [f"-L{d}" for d in cpp_extension.library_paths()] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"])
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

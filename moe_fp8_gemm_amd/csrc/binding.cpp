@@ -2,7 +2,7 @@
 //
 // A decoding step's calls work for a few microseconds, less than their arguments
 // cost to check and their outputs to allocate from Python (8 to 11 us a call; 3 to
-// 7 us from here).  Like the Python side of the binding this file only checks
+// 6 us from here).  Like the Python side of the binding this file only checks
 // tensors, allocates the outputs that are not passed in and calls the C ABI of
 // include/dgfp8.h with pointers, strides and the current stream of the tensors' device.
 // Wrong types raise TypeError, wrong shapes or values ValueError, and a status other
@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -110,10 +111,18 @@ void shape(const Args& a, const Tensor& t, const char* name, at::IntArrayRef wan
   TORCH_CHECK_VALUE(t.sizes() == want, a.call, ": ", name, " must have shape ", want, ", got ", t.sizes());
 }
 
+// A new contiguous tensor, without the dispatcher's share of at::empty (0.5 us of a
+// call's 4 to 7 for each tensor); with a row stride, a matrix whose rows begin that far
+// apart.
+Tensor fresh(at::IntArrayRef size, at::ScalarType type, const Tensor& like, int64_t row_stride = 0) {
+  if (row_stride > 0) return at::detail::empty_strided_cuda(size, {row_stride, 1}, type, like.device());
+  return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
+}
+
 // An output of this shape: the one passed in, or a new one.
 Tensor output(const Args& a, int i, const char* name, at::IntArrayRef want, at::ScalarType type, unsigned types,
               const Tensor& like) {
-  if (a.none(i)) return at::empty(want, like.options().dtype(type).requires_grad(false));
+  if (a.none(i)) return fresh(want, type, like);
   const Tensor& t = check(a, i, name, types, (int64_t)want.size());
   shape(a, t, name, want);
   return t;
@@ -198,6 +207,7 @@ PyObject* route_topk(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "route_topk"};
   const Tensor& x = check(a, 0, "logits", kF32 | kBF16 | kF16, 2);
+  const On on(x);
   const int topk = a.small(1, "topk");
   const int score = a.one_of(2, "score", "softmax", "sigmoid");
   const int64_t t = x.size(0), e = x.size(1);
@@ -210,7 +220,6 @@ PyObject* route_topk(PyObject*, PyObject* const* args, Py_ssize_t) {
   Tensor idx = output(a, 9, "indices", {t, topk}, at::kInt, kI32, x);
   Tensor w = output(a, 10, "weights", {t, topk}, at::kFloat, kF32, x);
   same_device(a, x, {&bias, &idx, &w});
-  const On on(x);
   if (!done(dg_route_topk(ptr(x), dtype_of(x), ld(x), bias.defined() ? f32(bias) : nullptr, ptr<int32_t>(idx), ld(idx),
                           ptr<float>(w), ld(w), t, (int)e, topk, a.small(4, "num_expert_groups"),
                           a.small(5, "topk_groups"), a.one_of(6, "group_score", "max", "top2"), score, a.truth(7),
@@ -225,6 +234,7 @@ PyObject* route_topk_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "route_topk_grad"};
   const Tensor& x = check(a, 0, "logits", kF32 | kBF16 | kF16, 2);
+  const On on(x);
   const Tensor& idx = check(a, 1, "indices", kI32, 2);
   const Tensor& g = check(a, 2, "dweights", kF32, 2);
   const int64_t t = x.size(0), e = x.size(1), topk = idx.size(1);
@@ -233,7 +243,6 @@ PyObject* route_topk_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
   TORCH_CHECK_VALUE(e <= INT32_MAX && topk <= INT32_MAX, a.call, ": too many columns");
   Tensor dx = output(a, 6, "dlogits", {t, e}, x.scalar_type(), type_bit(x), x);
   same_device(a, x, {&idx, &g, &dx});
-  const On on(x);
   if (!done(dg_route_topk_grad(ptr(x), dtype_of(x), ld(x), i32(idx), ld(idx), f32(g), ld(g), ptr(dx), ld(dx), t, (int)e,
                                (int)topk, a.one_of(3, "score", "softmax", "sigmoid"), a.truth(4),
                                (float)a.number(5, "scale"), on.stream),
@@ -260,13 +269,12 @@ PyObject* layout(PyObject* const* args, bool masked) {
     rows = a.none(2) ? dg_expert_layout_rows(t, (int)k, experts) : a.integer(2, "rows");
   }
   const On on(idx);
-  const auto opt = idx.options();
   const int64_t alloc = rows > 0 && rows <= INT32_MAX ? rows : 0;
-  Tensor m = masked ? Tensor() : at::empty({alloc}, opt);
-  Tensor row_slot = at::empty({alloc}, opt), slot_row = at::empty({t, k}, opt);
-  Tensor counts = at::empty({experts > 0 ? experts : 0}, opt);
+  Tensor m = masked ? Tensor() : fresh({alloc}, at::kInt, idx);
+  Tensor row_slot = fresh({alloc}, at::kInt, idx), slot_row = fresh({t, k}, at::kInt, idx);
+  Tensor counts = fresh({experts > 0 ? experts : 0}, at::kInt, idx);
   const size_t need = dg_expert_layout_workspace_size(t, (int)k, experts);
-  Tensor ws = need ? at::empty({(int64_t)need}, opt.dtype(at::kByte)) : Tensor();
+  Tensor ws = need ? fresh({(int64_t)need}, at::kByte, idx) : Tensor();
   void* wp = need ? ws.data_ptr() : nullptr;
   const dg_status st =
       masked ? dg_expert_layout_masked(i32(idx), ld(idx), t, (int)k, experts, max_m, ptr<int32_t>(counts),
@@ -297,8 +305,8 @@ PyObject* expert_layout_masked(PyObject*, PyObject* const* args, Py_ssize_t) {
 // int8 codes [rows, k]; new ones have rows that begin at 128-byte lines, which the
 // GEMM reads up to a third faster than rows that straddle them.
 Tensor int8_codes(const Args& a, int i, int64_t rows, int64_t k, const Tensor& like) {
-  if (!a.none(i) || k % 128 == 0) return output(a, i, "q", {rows, k}, at::kChar, kI8, like);
-  return at::empty({rows, (k + 127) / 128 * 128}, like.options().dtype(at::kChar)).narrow(1, 0, k);
+  if (a.none(i)) return fresh({rows, k}, at::kChar, like, (k + 127) / 128 * 128);
+  return output(a, i, "q", {rows, k}, at::kChar, kI8, like);
 }
 
 // fp32 scales of any strides
@@ -327,6 +335,7 @@ PyObject* dispatch_cast_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "dispatch_cast_fp8"};
   const Tensor& x = check(a, 0, "x", kF32 | kBF16, 2);
+  const On on(x);
   const Tensor& map = check(a, 1, "slot_row", kI32, 2);
   const int64_t t = x.size(0), k = x.size(1), topk = map.size(1);
   shape(a, map, "slot_row", {t, topk});
@@ -334,10 +343,9 @@ PyObject* dispatch_cast_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
   const int64_t rows = target_rows(a, 2, 4);
   Tensor q = output(a, 4, "q", {rows, k}, at::kFloat8_e4m3fn, kE4M3 | kU8, x);
   // new scales of one block lie beside each other along the rows, as the GEMM reads them best
-  Tensor sf = a.none(5) ? at::empty({k / 128, rows}, x.options().dtype(at::kFloat).requires_grad(false)).t()
+  Tensor sf = a.none(5) ? fresh({k / 128, rows}, at::kFloat, x).t()
                         : scales(a, 5, "sf", {rows, k / 128});
   same_device(a, x, {&map, &q, &sf});
-  const On on(x);
   if (!done(dg_dispatch_cast_fp8(ptr(x), dtype_of(x), ld(x), i32(map), ld(map), ptr(q), ld(q), ptr<float>(sf),
                                  sf.stride(0), sf.stride(1), t, (int)topk, rows, k, a.truth(3), on.stream),
             "dg_dispatch_cast_fp8"))
@@ -350,16 +358,16 @@ PyObject* dispatch_cast_int8(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "dispatch_cast_int8"};
   const Tensor& x = check(a, 0, "x", kF32 | kBF16, 2);
+  const On on(x);
   const Tensor& map = check(a, 1, "slot_row", kI32, 2);
   const int64_t t = x.size(0), k = x.size(1), topk = map.size(1);
   shape(a, map, "slot_row", {t, topk});
   TORCH_CHECK_VALUE(topk <= INT32_MAX, a.call, ": too many columns");
   const int64_t rows = target_rows(a, 2, 3);
   Tensor q = int8_codes(a, 3, rows, k, x);
-  Tensor sf = a.none(4) ? at::empty({rows}, x.options().dtype(at::kFloat).requires_grad(false))
+  Tensor sf = a.none(4) ? fresh({rows}, at::kFloat, x)
                         : scales(a, 4, "sf", {rows});
   same_device(a, x, {&map, &q, &sf});
-  const On on(x);
   if (!done(dg_dispatch_cast_int8(ptr(x), dtype_of(x), ld(x), i32(map), ld(map), ptr(q), ld(q), ptr<float>(sf),
                                   sf.stride(0), t, (int)topk, rows, k, on.stream),
             "dg_dispatch_cast_int8"))
@@ -372,12 +380,12 @@ PyObject* per_token_cast_int8(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "per_token_cast_int8"};
   const Tensor& x = check(a, 0, "x", kF32 | kBF16, 2);
+  const On on(x);
   const int64_t m = x.size(0), k = x.size(1);
   Tensor q = int8_codes(a, 1, m, k, x);
-  Tensor sf = a.none(2) ? at::empty({m}, x.options().dtype(at::kFloat).requires_grad(false))
+  Tensor sf = a.none(2) ? fresh({m}, at::kFloat, x)
                         : scales(a, 2, "sf", {m});
   same_device(a, x, {&q, &sf});
-  const On on(x);
   if (!done(dg_per_token_cast_int8(ptr(x), dtype_of(x), ld(x), ptr(q), ld(q), ptr<float>(sf), sf.stride(0), m, k,
                                    on.stream),
             "dg_per_token_cast_int8"))
@@ -392,6 +400,7 @@ PyObject* combine(PyObject*, PyObject* const* args, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Args a{args, "combine"};
   const Tensor& y = check(a, 0, "y", kBF16, 2);
+  const On on(y);
   const Tensor& map = check(a, 1, "slot_row", kI32, 2);
   const int64_t t = map.size(0), k = map.size(1), rows = y.size(0), h = y.size(1);
   TORCH_CHECK_VALUE(k <= INT32_MAX, a.call, ": too many columns");
@@ -402,7 +411,6 @@ PyObject* combine(PyObject*, PyObject* const* args, Py_ssize_t) {
   }
   Tensor out = output(a, 3, "out", {t, h}, at::kBFloat16, kBF16 | kF32, y);
   same_device(a, y, {&map, &w, &out});
-  const On on(y);
   if (!done(dg_combine(ptr(y), ld(y), i32(map), ld(map), w.defined() ? f32(w) : nullptr, w.defined() ? ld(w) : 0,
                        ptr(out), dtype_of(out), ld(out), t, (int)k, rows, h, on.stream),
             "dg_combine"))
@@ -416,6 +424,7 @@ PyObject* combine_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
   const Args a{args, "combine_grad"};
   const Tensor& g = check(a, 0, "dout", kBF16, 2);
   const Tensor& y = check(a, 1, "y", kBF16, 2);
+  const On on(y);
   const Tensor& map = check(a, 2, "slot_row", kI32, 2);
   const Tensor& back = check(a, 3, "row_slot", kI32, 1);
   const Tensor& w = check(a, 4, "weights", kF32, 2);
@@ -427,7 +436,6 @@ PyObject* combine_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
   Tensor dy = output(a, 5, "dy", {rows, h}, at::kBFloat16, kBF16, y);
   Tensor dw = output(a, 6, "dweights", {t, k}, at::kFloat, kF32, y);
   same_device(a, y, {&g, &map, &back, &w, &dy, &dw});
-  const On on(y);
   if (!done(dg_combine_grad(ptr(g), ld(g), ptr(y), ld(y), i32(map), ld(map), i32(back), f32(w), ld(w), ptr(dy), ld(dy),
                             ptr<float>(dw), ld(dw), t, (int)k, rows, h, on.stream),
             "dg_combine_grad"))

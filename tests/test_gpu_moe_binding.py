@@ -114,3 +114,24 @@ def test_current_stream_is_followed():
         idx, _ = dg.route_topk(x, 1)
     side.synchronize()
     assert bool((idx == 5).all())
+
+
+def test_new_outputs_are_ordinary_tensors():
+    """Outputs that the binding allocates belong to torch's allocator: device, autograd, views, streams, reuse."""
+    before = torch.cuda.memory_allocated()
+    idx, w = dg.route_topk(f32(64, 32), 4)
+    q, sf = dg.per_token_cast_int8(f32(5, 80))
+    assert idx.device == w.device == q.device == device() and not idx.requires_grad
+    assert q.shape == (5, 80) and q.stride() == (128, 1) and sf.shape == (5,)
+    assert torch.cuda.memory_allocated() > before
+    w2 = w.clone().requires_grad_()
+    (w2 * 2).sum().backward()
+    assert torch.equal(w2.grad, torch.full_like(w, 2))
+    w.requires_grad_()
+    assert (w * 3).sum().requires_grad
+    side = torch.cuda.Stream()
+    idx.record_stream(side)
+    assert idx.view(-1).sort().values.numel() == 256 and idx.t().contiguous().shape == (4, 64)
+    del idx, w, w2, q, sf
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() <= before
