@@ -11,7 +11,7 @@ namespace dgfp8 {
 // kDenseSplitK: dense GEMM whose K range is split over several workgroups per
 // output tile (small M); partial sums go through a workspace.
 // kContiguousSplitK: the contiguous GEMM on the 128-row blocks listed on the
-// device (contig_mode 2), with a K split the kernel derives from the number of
+// device (contig_mode 2 or 3), with a K split the kernel derives from the number of
 // listed blocks (see contig_split_units).
 enum Variant : int { kDense = 0, kContiguous = 1, kMasked = 2, kDenseSplitK = 3, kContiguousSplitK = 4 };
 
@@ -62,13 +62,13 @@ struct GemmParams {
 // Largest number of 128-row blocks (m_total / 128) a paired contiguous plan takes.
 constexpr int kMaxContigPairBlocks = 2048;
 
-// Kernel instances the host can pick (see gemm_fp8.hip for the tile shapes).
+// Kernel instances the host can pick (see gemm_core.h for the tile shapes).
 enum GemmInstance : int {
   kInstLarge = 0,     // 128 x 256 output tiles, 8 waves, 3-stage LDS pipeline
   kInstMid = 1,       // 128 x 128 output tiles, 8 waves, 3-stage LDS pipeline
   kInstHuge = 2,      // 256 x 256 output tiles, 8 waves, 2-stage LDS pipeline (dense, masked)
   kInstSkinny128 = 3, // 128 x 64 output tiles, 8 waves, 4-stage LDS pipeline (small M, usually split over K)
-  kInstSkinny64 = 4,  // 64 x 64 output tiles, 8 waves, 4-stage LDS pipeline (M <= 64, usually split over K)
+  kInstSkinny64 = 4,  // 64 x 64 output tiles, 8 waves, 4-stage LDS pipeline (M <= 64, usually split over K; int8: masked too)
   kInstDecode = 5,    // 64 x 256 output tiles, 8 waves side by side, 3-stage LDS pipeline (masked, few rows)
   kInstTall = 6,      // 192 x 256 output tiles, 8 waves, 2-stage LDS pipeline (dense, fills the device where 256x256 does not)
   kNumInstances

@@ -92,12 +92,20 @@ struct SfCfg : Base {
 // that A and B share serves an exact sum), at the rate of one FP8 MFMA of the
 // block.  No scale moves through the K loop.  A K block cut short by the end of K
 // (k % 128 != 0) runs once per tile outside the pipeline (short_block).
+//   Measured: 4096x7168x16384 380 us (2.5 POPS) on 256x256 tiles, bound by the MFMAs at
+// the clock they leave (4096x4096x8192: 109 us, 98 without the K loop's loads);
+// 777x2112x7168 24 us and 512x7168x2048 15 us on 128x128 tiles, bound by a K block's
+// chain of barrier, LDS reads and MFMAs (0.53 us of it where 256 CUs share the MFMAs'
+// 0.2; 64 blocks 42 us, 35 without loads).  A barrier every other K block (5 to 20%
+// slower) and 4 waves of 64x64 in place of 8 (a third fewer LDS reads, 0 to 10%
+// slower) did not shorten it.  Rows that straddle 128-byte lines double the requests
+// to L2: 777x2112x7152 with both operands packed 32 us.
 template <class Base>
 struct Int8Cfg : Base {
   static constexpr bool kInt8 = true;
   static constexpr int kLoadsPerStage = Base::kLoadsPerStage - 1;   // no scales
   static_assert(Base::BM + Base::BN <= Base::kThreads, "one thread fetches each of a tile's scales");
-  // 64-row tiles serve problems of at most 64 rows (a group), so one workgroup
+  // 64-row tiles serve problems of about 64 rows (a group), so as a rule one workgroup
   // reads a row of B, once.  Masked decode of 16 groups of 4096x7168 (470 MB): 86 us
   // through L2, 78 us past it; 64x4096x7168 13.2 to 12.6 us.
   static constexpr bool kStreamB = Base::BM == 64;
