@@ -9,14 +9,14 @@
 // the order in which workgroups or atomics run.
 //
 // Little is read and written (12 bytes a slot, 8 a row), so the time is launches
-// and dependent steps.  Up to 1024 slots one launch does it all: every workgroup
+// and dependent steps.  Up to 3072 slots one launch does it all: every workgroup
 // counts all slots by itself, the first writes the slots' rows, and all share the
 // rows that hold nothing.  Beyond, a first launch counts each workgroup's slots
 // per expert, and in the second each workgroup adds up the counts before its
 // own.  Inside a workgroup each wave ranks its consecutive slots 64 at a time
 // with ballots over the bits of the expert number.
-// Measured, 256 experts, top 8: 64 tokens 4.8 us (one launch), 512 tokens 8.0 us,
-// 4096 tokens 8.7 us, 32768 tokens 16 us.
+// Measured, 256 experts, top 8: 1 token 4.2 us, 64 tokens 4.8, 256 tokens 6.9 (two launches: 9.1), 320
+// tokens 8.1 (8.4), 512 tokens 8.6 (one launch: 9.9), 4096 tokens 8.7, 32768 tokens 16.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
   const int bits = 32 - __builtin_clz(p.experts);   // experts <= 2^bits - 1
   int expert[kSteps], rank[kSteps];
 #pragma unroll
+  for (int i = 0; i < kSteps; ++i) expert[i] = expert_at(p, s0 + i * 64 + lane);
+#pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int e = expert_at(p, s0 + i * 64 + lane);
-    expert[i] = e;
+    const int e = expert[i];
     uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
     if (same == 0) {   // a whole run past the end
       rank[i] = 0;
@@ -202,11 +203,18 @@ hipError_t count_and_place(const LayoutParams& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
-  if (p.blocks == 1) {
-    // one workgroup for each 4096 rows, which they share the clearing of
+  if (p.slots <= 3 * kThreads) {
+    // one workgroup for each 4096 rows and each 32 experts, which they share the clearing of
     int64_t grid = (p.rows + 4095) / 4096;
-    grid = grid < 1 ? 1 : grid > 64 ? 64 : grid;
-    place<false, 1>(p, (int)grid, stream);
+    if (grid < (p.experts + 31) / 32) grid = (p.experts + 31) / 32;
+    if (grid > 64) grid = 64;
+    if (p.slots <= kThreads) {
+      place<false, 1>(p, (int)grid, stream);
+    } else if (p.slots <= 2 * kThreads) {
+      place<false, 2>(p, (int)grid, stream);
+    } else {
+      place<false, 3>(p, (int)grid, stream);
+    }
     return hipGetLastError();
   }
   return layout_block_slots(p.slots) == kThreads ? count_and_place<1>(p, stream) : count_and_place<4>(p, stream);

@@ -61,6 +61,12 @@ def test_layouts(t, k, e):
         assert np.array_equal(lay.row_slot.cpu().numpy(), row_slot)
 
 
+@pytest.mark.parametrize("t,k,e", [(129, 8, 256), (256, 8, 256), (257, 8, 700), (1025, 1, 5), (384, 8, 60), (385, 8, 60),
+                                   (3073, 1, 1), (1024, 3, 1024)])
+def test_layouts_around_the_sizes_of_one_launch(t, k, e):
+    test_layouts(t, k, e)
+
+
 def test_layout_of_one_crowded_expert_and_of_strided_indices():
     idx = np.full((3000, 3), -1, np.int32)
     idx[:, 1] = 5
