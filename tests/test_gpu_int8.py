@@ -57,6 +57,20 @@ def test_cast(m, k, dtype):
     assert np.array_equal(q.cpu().numpy(), oq)
 
 
+@pytest.mark.parametrize("m,k", [(3, 2048), (3, 2064), (2, 4096), (5, 4112), (2, 16384), (2, 16400)])
+def test_cast_rows_around_what_registers_hold(m, k):
+    test_cast(m, k, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_cast_ties_and_ends(dtype):
+    """A maximum of 127 makes the scale 1: halves go to the even code, and the ends stay at +-127."""
+    x = torch.tensor([127.0, -127.0, 0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 126.5, -126.5, 63.5, -64.5, 0.0, -0.0, 0.4375, 126.0])
+    q, s = dg.per_token_cast_int8(x.to(dtype).view(1, 16).to(device()))
+    assert float(s) == 1.0
+    assert q.cpu().view(-1).tolist() == [127, -127, 0, 2, 2, 0, -2, -2, 126, -126, 64, -64, 0, 0, 0, 126]
+
+
 def test_cast_strides_and_bad_rows():
     x = torch.randn((6, 160), device=device())
     x[2, 9], x[4, 3] = float("nan"), float("inf")

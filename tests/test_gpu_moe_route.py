@@ -188,3 +188,81 @@ def test_gradient_of_unused_slots():
             dx = dg.route_topk_grad(x, idx, g, score=score, renormalize=renormalize).cpu().numpy()
             want = moe.route_grad(x.cpu().numpy(), host_idx, np.nan_to_num(g.cpu().numpy()), score, renormalize)
             assert np.abs(dx - want).max() <= G_TOL * 4 and np.all(dx[2] == 0)
+
+
+# ---------------------------------------------------------------- many tokens
+# Over 64 experts few tokens take a wave each; these run the same rows among many, four to a wave,
+# where neighbours differ in what they need, against the same oracle and bounds.
+
+MANY = 8200
+
+
+def check_among_many(x, topk, what, bias=None, grad=True, least_clear=0.95, **kw):
+    """check() of x's rows repeated to more tokens than a wave each is used for."""
+    n, reps = x.shape[0], -(-MANY // x.shape[0])
+    host = x.float().cpu().numpy().astype(np.float64)
+    gkw = {k: v for k, v in kw.items() if k in ("score", "renormalize", "scale")}
+    okw = dict(kw)
+    if "num_expert_groups" in okw:
+        okw["groups"] = okw.pop("num_expert_groups")
+    many = x.repeat(reps, 1)
+    idx, w = dg.route_topk(many, topk, bias=bias, **kw)
+    want_idx, want_w, margin = moe.route(host, topk, bias=None if bias is None else bias.cpu().numpy(), **okw)
+    clear = margin > CLOSE
+    assert clear.mean() >= least_clear or n < 20, f"{what}: {clear.mean()} of the rows are clear"
+    got_idx = idx.cpu().numpy().reshape(reps, n, topk)[:, clear]
+    got_w = w.cpu().numpy().astype(np.float64).reshape(reps, n, topk)[:, clear]
+    assert (got_idx == want_idx[clear]).all(), f"{what}: indices differ"
+    ok = np.isclose(got_w, np.broadcast_to(want_w[clear], got_w.shape), rtol=W_TOL, atol=1e-37, equal_nan=True)
+    assert ok.all(), f"{what}: weights differ at {np.argwhere(~ok)[:4].tolist()}"
+    if not grad:
+        return
+    g = torch.from_numpy(np.random.default_rng(1).standard_normal((n, topk)).astype(np.float32)).to(device())
+    dx = dg.route_topk_grad(many, idx, g.repeat(reps, 1), **gkw).float().cpu().numpy().astype(np.float64)
+    want = moe.route_grad(host, want_idx, g.cpu().numpy(), **gkw)
+    bound = G_TOL * np.abs(g.cpu().numpy()).max(1, keepdims=True) * gkw.get("scale", 1.0)
+    if x.dtype != torch.float32:    # and one rounding to the type: half its spacing, or of its smallest numbers
+        info = torch.finfo(x.dtype)
+        bound = bound + np.abs(want) * info.eps / 2 + info.smallest_normal * info.eps
+    sane = np.isfinite(host).all(1) | (host == -np.inf).any(1) & ~np.isnan(host).any(1)
+    rows = sane & clear
+    bad = ~(np.abs(dx.reshape(reps, n, -1)[:, rows] - want[rows]) <= bound[rows])
+    assert not bad.any(), f"{what}: gradient off at {np.argwhere(bad)[:4].tolist()}"
+
+
+@pytest.fixture
+def among_many(monkeypatch):
+    monkeypatch.setitem(globals(), "check", check_among_many)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("t,e,k", [(37, 65, 7), (40, 72, 6), (51, 128, 16), (31, 160, 8), (64, 255, 1), (65, 256, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_sizes_among_many(among_many, t, e, k, dtype, score):
+    test_sizes(t, e, k, dtype, score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("e,groups,topk_groups,k", [(72, 6, 5, 8), (128, 8, 1, 4), (160, 8, 3, 6), (256, 8, 4, 8),
+                                                    (256, 32, 7, 8), (256, 64, 64, 3)])
+def test_groups_and_bias_among_many(among_many, score, group_score, e, groups, topk_groups, k):
+    test_groups_and_bias(score, group_score, e, groups, topk_groups, k)
+
+
+@pytest.mark.parametrize("e", [100, 256])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_ties_among_many(among_many, e, score):
+    test_ties_go_to_the_lowest_number(e, score)
+
+
+@pytest.mark.parametrize("e,groups", [(120, 4), (256, 1), (256, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masks_among_many(among_many, e, groups, score):
+    test_masked_and_extreme_logits(e, groups, score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [90, 256])
+def test_nan_among_many(among_many, score, e):
+    test_nan_marks_the_token_and_no_other(score, e)
