@@ -210,10 +210,11 @@ DG_EXPORT dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y
   if (rows > 0 && h > 0) {
     if ((st = check_rows(y, ldy, h, 2)) != DG_SUCCESS) return st;
     if ((st = check_rows(dy, lddy, h, 2)) != DG_SUCCESS) return st;
-    if (!row_slot) return DG_ERROR_INVALID_VALUE;
-    if (!aligned(row_slot, 4)) return DG_ERROR_NOT_SUPPORTED;
   }
   if (tokens == 0 && (rows == 0 || h == 0)) return DG_SUCCESS;
+  // read for every row, also where h == 0 leaves nothing to clear
+  if (rows > 0 && !row_slot) return DG_ERROR_INVALID_VALUE;
+  if (!aligned(row_slot, 4)) return DG_ERROR_NOT_SUPPORTED;
   if (tokens + rows / 64 >= 2 * kMaxTokens) return DG_ERROR_NOT_SUPPORTED;   // grid
   CombineGradParams p{dout, ldo, y, ldy, slot_row, lds, row_slot, weights, ldw, dy, lddy, dweights, lddw,
                       tokens, rows, h, topk};

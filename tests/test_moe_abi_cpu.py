@@ -139,6 +139,13 @@ def test_combine_grad(kw, status):
     assert call(lib.dg_combine_grad, COMBINE_GRAD, **kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(row_slot=None), INVALID), (dict(row_slot=P + 2), UNSUPPORTED), (dict(row_slot=None, tokens=0), OK)])
+def test_combine_grad_without_columns(kw, status):
+    """h == 0: the weights' gradients are still written, so the map is checked with the rest."""
+    assert call(lib.dg_combine_grad, dict(COMBINE_GRAD, h=0), **kw) == status
+
+
 CAST8 = dict(x=P, dtype=1, ldx=256, q=P, ldq=256, sf=P, sf_s=1, m=4, k=256, stream=None)
 
 
