@@ -617,9 +617,10 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
 #pragma unroll
   for (int k = 0; k < kSlots; ++k) {
     if (chosen[k] < 0) continue;
-    float ds = g[k];
-    if (p.renormalize) ds = sum == 0.0f ? 0.0f : (ds - dot / sum) / sum;
-    mine[chosen[k]] = softmax ? ds * score[k] : ds * score[k] * (1.0f - score[k]);
+    float dx = g[k] * score[k];
+    // shares before gradients: the sum may be subnormal, and its reciprocal out of range
+    if (p.renormalize) dx = sum == 0.0f ? 0.0f : (g[k] - dot / sum) * (score[k] / sum);
+    mine[chosen[k]] = softmax ? dx : dx * (1.0f - score[k]);
   }
   wave_sync();
   if (!live) return;

@@ -266,3 +266,19 @@ def test_masks_among_many(among_many, e, groups, score):
 @pytest.mark.parametrize("e", [90, 256])
 def test_nan_among_many(among_many, score, e):
     test_nan_marks_the_token_and_no_other(score, e)
+
+
+# ---------------------------------------------------------------- gradients at the ends of fp32
+
+@pytest.mark.parametrize("t", [6, 3000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_renormalised_scores_near_underflow(score, t):
+    """Sigmoids of logits below -87.4 are subnormal: they are no divisors for a gradient, their shares are.  A
+    subnormal score of 3e-39 or more is right to 2.4e-7 of itself, within what G_TOL allows for a score."""
+    x = draw(t, 128, torch.float32, 9) / 100
+    x[0::6] -= 88.4
+    x[1::6] -= 87.5
+    x[2::6] -= 80.0
+    x[3::6, ::2] -= 88.4                                 # ordinary logits beside them
+    x[4::6, 1:] -= 88.4
+    check(x, 6, "scores near underflow", score=score, renormalize=True, scale=16.0)
