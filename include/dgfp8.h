@@ -587,6 +587,9 @@ dg_status dg_route_topk(const void* logits, int dtype, int64_t ld, const float* 
  *             an index outside [0, experts) marks an unused slot
  *   dweights  device, fp32 [tokens, topk], row stride ldw
  *   dlogits   device, dtype [tokens, experts], row stride ldd; must not overlap logits
+ * Under plain softmax every score depends on every logit: a token with a NaN (or +inf) logit
+ * gets a row of NaN.  In the other forms only the chosen experts' logits enter, so such a logit
+ * of an expert that is not chosen leaves the row finite, though the token's weights are NaN.
  * Limits and errors as dg_route_topk (ldd < experts -> DG_ERROR_INVALID_VALUE).
  */
 dg_status dg_route_topk_grad(const void* logits, int dtype, int64_t ld, const int32_t* indices, int64_t ldi,

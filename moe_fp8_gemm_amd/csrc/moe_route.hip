@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradParams p)
   float out[kVals];
 #pragma unroll
   for (int i = 0; i < kVals; ++i) out[i] = mine[e0 + i / kPer * kLanes * kPer + i % kPer];
-  if (dense && total > 0.0f) {
+  if (dense && total != 0.0f) {   // 0: no expert has a score; NaN (from the logits): no gradient is known
     const float share = inv * dot;
 #pragma unroll
     for (int i = 0; i < kVals; ++i) out[i] -= x[i] * share;

@@ -61,6 +61,7 @@ def route_topk_grad(logits: torch.Tensor, indices: torch.Tensor, dweights: torch
 
     indices int32 and dweights fp32 are [tokens, topk]; the other arguments as they were given to ``route_topk``.
     The choice of experts is held fixed, so a bias or groups do not enter.
+    Under plain softmax (not renormalised) a NaN logit makes its token's row NaN; otherwise only the chosen logits enter.
     """
     return _native.route_topk_grad(logits, indices, dweights, score, renormalize, scale, dlogits)
 

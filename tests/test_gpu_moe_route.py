@@ -282,3 +282,28 @@ def test_gradient_of_renormalised_scores_near_underflow(score, t):
     x[3::6, ::2] -= 88.4                                 # ordinary logits beside them
     x[4::6, 1:] -= 88.4
     check(x, 6, "scores near underflow", score=score, renormalize=True, scale=16.0)
+
+
+@pytest.mark.parametrize("t", [6, 5000])
+@pytest.mark.parametrize("score,renormalize", [("softmax", False), ("softmax", True), ("sigmoid", False),
+                                               ("sigmoid", True)])
+def test_gradient_of_a_logit_without_a_score(score, renormalize, t):
+    """Plain softmax: every score of the token depends on the logit, so its whole row is NaN.  The other forms depend
+    on the chosen logits alone, and a logit without a score is never chosen."""
+    x = draw(t, 160, torch.float32, 10)
+    x[0, 7] = float("nan")
+    x[1, 159] = -float("nan")
+    if score == "softmax":
+        x[3, 2] = float("inf")
+    idx, w = dg.route_topk(x, 6, score=score, renormalize=renormalize)
+    lost = torch.isnan(w).all(1).cpu().numpy()
+    assert lost.tolist() == [True, True, False, score == "softmax"] + [False] * (t - 4)
+    g = torch.randn((t, 6), generator=torch.Generator().manual_seed(1)).to(device())
+    dx = dg.route_topk_grad(x, idx, g, score=score, renormalize=renormalize, scale=2.5).cpu().numpy()
+    want = moe.route_grad(x.cpu().numpy(), idx.cpu().numpy(), g.cpu().numpy(), score, renormalize, 2.5)
+    if score == "softmax" and not renormalize:
+        want[lost] = np.nan
+    assert np.array_equal(np.isnan(dx), np.isnan(want))
+    ok = np.isnan(want).any(1)
+    bound = G_TOL * 2.5 * np.abs(g.cpu().numpy()).max(1, keepdims=True)
+    assert np.all(np.abs(dx - want)[~ok] <= np.broadcast_to(bound, dx.shape)[~ok])
