@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) layout_count_kernel(LayoutParams p) 
 // kSteps: runs of 64 slots of a wave.
 template <bool kCounted, int kExperts, int kSteps>
 __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) {
-  __shared__ int wave_count[kWaves][kExperts];   // slots of an expert in each wave; then the row of the wave's first
+  __shared__ int wave_count[kWaves][kExperts];   // slots of an expert in each wave; then the slots before the wave's
   __shared__ int wave_sum[kWaves];
   __shared__ int start[kExperts];                // first row of an expert
   __shared__ int held[kExperts];                 // its rows that hold a slot
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
     start[e_mine] = first;
     held[e_mine] = masked ? (int)(mine < limit ? mine : limit) : mine;
     if (blockIdx.x == 0) p.counts[e_mine] = held[e_mine];
-    int run = first + earlier;
+    int run = earlier;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const int c = wave_count[w][e_mine];
@@ -151,9 +151,8 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
       const int e = expert[i];
       int row = -1;
       if (e >= 0) {
-        row = wave_count[wave][e] + rank[i];
-        const int64_t limit = masked ? (int64_t)(e + 1) * p.max_m : p.rows;
-        if (row >= limit) row = -1;   // no room: the slot is dropped
+        const int64_t in_expert = wave_count[wave][e] + rank[i], at = start[e] + in_expert;
+        if (masked ? in_expert < p.max_m : at < p.rows) row = (int)at;   // else no room: the slot is dropped
       }
       p.slot_row[s] = row;
       if (row >= 0) {

@@ -246,3 +246,18 @@ def test_layer_steps_in_a_graph_and_on_another_stream():
         want = step()
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------- layouts of many slots
+
+def test_masked_rows_at_the_end_of_int32():
+    """The last expert's slots outnumber its rows, which end just below 2^31: every slot past them is dropped as -1."""
+    t, e, max_m = 2_100_000, 1024, 2_097_151
+    assert (e - 1) * max_m + t > 1 << 31 > e * max_m
+    lay = dg.expert_layout_masked(torch.full((t, 1), e - 1, dtype=torch.int32, device=device()), e, max_m)
+    want = torch.arange(t, dtype=torch.int64, device=device()) + (e - 1) * max_m
+    want[max_m:] = -1
+    assert torch.equal(lay.slot_row[:, 0].long(), want)
+    assert lay.counts.tolist() == [0] * (e - 1) + [max_m]
+    assert bool((lay.row_slot[:(e - 1) * max_m] == -1).all())
+    assert torch.equal(lay.row_slot[(e - 1) * max_m:], torch.arange(max_m, dtype=torch.int32, device=device()))
