@@ -123,7 +123,7 @@ DG_EXPORT int64_t dg_expert_layout_rows(int64_t tokens, int topk, int experts) {
 DG_EXPORT size_t dg_expert_layout_workspace_size(int64_t tokens, int topk, int experts) {
   if (!layout_sizes_ok(tokens, topk, experts)) return 0;
   const int64_t blocks = ceil_div(tokens * topk, layout_block_slots(tokens * topk));
-  return blocks > 1 ? (size_t)blocks * experts * sizeof(int32_t) : 0;
+  return blocks > 1 ? (size_t)layout_hist_rows(blocks) * experts * sizeof(int32_t) : 0;
 }
 
 DG_EXPORT dg_status dg_expert_layout_contiguous(const int32_t* indices, int64_t ldi, int64_t tokens, int topk,

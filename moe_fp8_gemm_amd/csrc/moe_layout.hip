@@ -13,10 +13,12 @@
 // counts all slots by itself, the first writes the slots' rows, and all share the
 // rows that hold nothing.  Beyond, a first launch counts each workgroup's slots
 // per expert, and in the second each workgroup adds up the counts before its
-// own.  Inside a workgroup each wave ranks its consecutive slots 64 at a time
+// own; past kSumBlocks workgroups, where that grows with their square, a launch between the
+// two replaces the counts by their sums.  Inside a workgroup each wave ranks its consecutive slots 64 at a time
 // with ballots over the bits of the expert number.
 // Measured, 256 experts, top 8: 1 token 4.2 us, 64 tokens 4.8, 256 tokens 6.9 (two launches: 9.1), 320
-// tokens 8.1 (8.4), 512 tokens 8.6 (one launch: 9.9), 4096 tokens 8.7, 32768 tokens 16.
+// tokens 8.1 (8.4), 512 tokens 8.6 (one launch: 9.9), 4096 tokens 8.6, 32768 tokens 17, 1 M
+// tokens 124.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -52,6 +54,40 @@ __global__ void __launch_bounds__(kThreads) layout_count_kernel(LayoutParams p) 
   }
   __syncthreads();
   if ((int)threadIdx.x < p.experts) p.hist[(int64_t)blockIdx.x * p.experts + threadIdx.x] = count[threadIdx.x];
+}
+
+// Each workgroup's counts become the sums over the workgroups before it, and the row behind the last
+// the sums over all.  A workgroup takes 64 experts; each of its waves adds up a run of rows, then
+// walks it again from the sum of the earlier runs.
+__global__ void __launch_bounds__(kThreads) layout_sum_kernel(LayoutParams p) {
+  __shared__ int run_sum[kWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
+  const int per = (p.blocks + kWaves - 1) / kWaves;
+  const int b0 = wave * per, b1 = min(b0 + per, p.blocks);
+  int sum = 0;
+  if (e < p.experts) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) sum += p.hist[(int64_t)b * p.experts + e];
+  }
+  run_sum[wave][lane] = sum;
+  __syncthreads();
+  if (e >= p.experts) return;
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += run_sum[w][lane];
+  if (wave == kWaves - 1) p.hist[(int64_t)p.blocks * p.experts + e] = before + sum;
+  constexpr int kBatch = 8;   // counts in flight
+  for (int b = b0; b < b1; b += kBatch) {
+    int c[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) c[i] = b + i < b1 ? p.hist[(int64_t)(b + i) * p.experts + e] : 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (b + i < b1) p.hist[(int64_t)(b + i) * p.experts + e] = before;
+      before += c[i];
+    }
+  }
 }
 
 // kCounted: layout_count_kernel has filled p.hist, and each workgroup places its
@@ -102,11 +138,16 @@ __global__ void __launch_bounds__(kThreads) layout_place_kernel(LayoutParams p) 
   int mine = 0, earlier = 0;   // of expert e_mine: all slots, slots of earlier workgroups
   if (e_mine < p.experts) {
     if constexpr (kCounted) {
+      if (p.blocks > kSumBlocks) {
+        mine = p.hist[(int64_t)p.blocks * p.experts + e_mine];
+        earlier = p.hist[(int64_t)blockIdx.x * p.experts + e_mine];
+      } else {
 #pragma unroll 8
-      for (int b = 0; b < p.blocks; ++b) {
-        const int c = p.hist[(int64_t)b * p.experts + e_mine];
-        mine += c;
-        earlier += b < (int)blockIdx.x ? c : 0;
+        for (int b = 0; b < p.blocks; ++b) {
+          const int c = p.hist[(int64_t)b * p.experts + e_mine];
+          mine += c;
+          earlier += b < (int)blockIdx.x ? c : 0;
+        }
       }
     } else {
 #pragma unroll
@@ -193,8 +234,12 @@ void place(const LayoutParams& p, int grid, hipStream_t stream) {
 template <int kSteps>
 hipError_t count_and_place(const LayoutParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((layout_count_kernel<kSteps>), dim3(p.blocks), dim3(kThreads), 0, stream, p);
-  const hipError_t err = hipGetLastError();
+  hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  if (p.blocks > kSumBlocks) {
+    hipLaunchKernelGGL(layout_sum_kernel, dim3((p.experts + 63) / 64), dim3(kThreads), 0, stream, p);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
   place<true, kSteps>(p, p.blocks, stream);
   return hipGetLastError();
 }

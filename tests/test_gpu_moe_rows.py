@@ -250,6 +250,17 @@ def test_layer_steps_in_a_graph_and_on_another_stream():
 
 # ---------------------------------------------------------------- layouts of many slots
 
+@pytest.mark.parametrize("t,k,e", [(8193, 8, 256), (9001, 8, 1000), (70001, 1, 7), (21846, 3, 64)])
+def test_layouts_past_64_workgroups(t, k, e):
+    test_layouts(t, k, e)
+
+
+@pytest.mark.parametrize("t,k,e", [(131073, 3, 256), (49153, 8, 1000), (400_001, 1, 5)])
+def test_layouts_whose_counts_are_summed_apart(t, k, e):
+    """Past 96 workgroups of 4096 slots."""
+    test_layouts(t, k, e)
+
+
 def test_masked_rows_at_the_end_of_int32():
     """The last expert's slots outnumber its rows, which end just below 2^31: every slot past them is dropped as -1."""
     t, e, max_m = 2_100_000, 1024, 2_097_151
@@ -261,3 +272,22 @@ def test_masked_rows_at_the_end_of_int32():
     assert lay.counts.tolist() == [0] * (e - 1) + [max_m]
     assert bool((lay.row_slot[:(e - 1) * max_m] == -1).all())
     assert torch.equal(lay.row_slot[(e - 1) * max_m:], torch.arange(max_m, dtype=torch.int32, device=device()))
+
+
+def test_layout_time_grows_with_the_slots():
+    """Four times the slots take about four times as long, not sixteen times."""
+    def least(t):
+        idx = torch.randint(0, 256, (t, 8), generator=torch.Generator(device=device()).manual_seed(1), device=device(),
+                            dtype=torch.int32)
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            dg.expert_layout_masked(idx, 256, 1 << 16)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    small, large = least(1 << 21), least(1 << 23)
+    assert large < 8 * small, f"{small} ms, then {large} ms"
