@@ -612,7 +612,7 @@ dg_status dg_route_topk_grad(const void* logits, int dtype, int64_t ld, const in
  *   slot_row  device, int32 [tokens, topk], dense: row of the slot, or -1
  *   counts    device, int32 [experts]: slots of each expert
  *   ws        device, 16-byte aligned, dg_expert_layout_workspace_size() bytes
- *             (contents do not matter; NULL where that is 0)
+ *             (contents do not matter); not used, and may be NULL, up to 3072 slots
  * Limits: experts <= 1024, topk <= 64, tokens * topk <= 2^30, rows < 2^31.
  * Errors: rows % 128 != 0 -> DG_ERROR_MISALIGNED_LAYOUT; null pointers, negative
  * sizes, ldi < topk, ws too small -> DG_ERROR_INVALID_VALUE; beyond the limits, or
@@ -626,7 +626,7 @@ dg_status dg_expert_layout_contiguous(const int32_t* indices, int64_t ldi, int64
  * multiple of 128); 0 for sizes outside the limits. */
 int64_t dg_expert_layout_rows(int64_t tokens, int topk, int experts);
 
-/* Workspace bytes of the two layout calls: 0 up to 1024 slots. */
+/* Workspace bytes that serve the two layout calls: 0 up to 1024 slots. */
 size_t dg_expert_layout_workspace_size(int64_t tokens, int topk, int experts);
 
 /*

@@ -61,7 +61,8 @@ dg_status layout(const int32_t* indices, int64_t ldi, int64_t tokens, int topk, 
   if (!aligned(indices, 4) || !aligned(m_indices, 4) || !aligned(row_slot, 4) || !aligned(slot_row, 4) ||
       !aligned(counts, 4) || !aligned(ws, 16))
     return DG_ERROR_NOT_SUPPORTED;
-  const size_t need = dg_expert_layout_workspace_size(tokens, topk, experts);
+  const size_t need =
+      tokens * topk <= kOneLaunchSlots ? 0 : dg_expert_layout_workspace_size(tokens, topk, experts);
   if (need > 0 && (!ws || ws_bytes < need)) return DG_ERROR_INVALID_VALUE;
   LayoutParams p{};
   p.indices = indices; p.ldi = ldi;

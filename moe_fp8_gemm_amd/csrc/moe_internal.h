@@ -62,6 +62,8 @@ struct LayoutParams {
   int32_t* hist;                  // [blocks, experts] (summed: [blocks + 1, experts]): workspace of large calls
   int blocks;                     // workgroups that share the slots
 };
+// One launch lays out this many slots, without a workspace (see moe_layout.hip).
+constexpr int64_t kOneLaunchSlots = 3 * 1024;
 // Slots of one workgroup: 1024 each, so that the work spreads; past 64 workgroups
 // 4096, so that the counts each of them adds up stay few.
 constexpr int64_t layout_block_slots(int64_t slots) { return slots <= 65536 ? 1024 : 4096; }

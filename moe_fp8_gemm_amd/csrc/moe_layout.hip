@@ -247,7 +247,8 @@ hipError_t count_and_place(const LayoutParams& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
-  if (p.slots <= 3 * kThreads) {
+  static_assert(kOneLaunchSlots == 3 * kThreads, "steps of the one launch");
+  if (p.slots <= kOneLaunchSlots) {
     // one workgroup for each 4096 rows and each 32 experts, which they share the clearing of
     int64_t grid = (p.rows + 4095) / 4096;
     if (grid < (p.experts + 31) / 32) grid = (p.experts + 31) / 32;

@@ -291,3 +291,22 @@ def test_layout_time_grows_with_the_slots():
 
     small, large = least(1 << 21), least(1 << 23)
     assert large < 8 * small, f"{small} ms, then {large} ms"
+
+
+def test_small_layouts_take_no_workspace():
+    """Up to 3072 slots the calls use none and do not ask for one."""
+    for t in (128, 129, 384):
+        idx = torch.from_numpy(routing(t, 8, 60, seed=t)).to(device())
+        rows = dg.expert_layout_rows(t, 8, 60)
+        new = lambda *size: torch.full(size, -7, dtype=torch.int32, device=device())  # noqa: E731
+        m, row_slot, slot_row, counts = new(rows), new(rows), new(t, 8), new(60)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert dg.lib.dg_expert_layout_contiguous(idx.data_ptr(), 8, t, 8, 60, rows, m.data_ptr(), row_slot.data_ptr(),
+                                                  slot_row.data_ptr(), counts.data_ptr(), None, 0, stream) == 0
+        for got, want in zip((m, row_slot, slot_row, counts), moe.layout_contiguous(idx.cpu().numpy(), 60, rows)):
+            assert np.array_equal(got.cpu().numpy(), want)
+        row_slot = new(60 * 16)
+        assert dg.lib.dg_expert_layout_masked(idx.data_ptr(), 8, t, 8, 60, 16, counts.data_ptr(), row_slot.data_ptr(),
+                                              slot_row.data_ptr(), None, 0, stream) == 0
+        for got, want in zip((row_slot, slot_row, counts), moe.layout_masked(idx.cpu().numpy(), 60, 16)):
+            assert np.array_equal(got.cpu().numpy(), want)
