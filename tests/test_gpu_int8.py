@@ -346,3 +346,39 @@ def test_operands_near_the_32_bit_offset_limit():
     st = dg.lib.dg_int8_gemm_nt(qa.data_ptr(), ld, sa.data_ptr(), 1, qa.data_ptr(), ld, sa.data_ptr(), 1, d.data_ptr(), 0,
                                 1 << 20, rows + 1, 40, k, None, 0, None)
     assert st == dg.DG_ERROR_NOT_SUPPORTED
+
+
+# ---------------------------------------------------------------- NaN and infinities
+
+def exactly(got, want):
+    """NaN in the same places, everything else equal, infinities among it."""
+    got = got.cpu()
+    return torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~got.isnan()], want[~want.isnan()])
+
+
+@pytest.mark.parametrize("dtype", OUT)
+@pytest.mark.parametrize("m,n,k", [(3, 40, 256), (8, 520, 1040), (64, 129, 272), (130, 264, 512), (300, 2112, 1424)])
+def test_infinite_and_nan_scales_exactly(m, n, k, dtype):
+    qa, sa, qb, sb = operands(m, n, k, seed=m)
+    sa[0], sa[1], sa[2] = np.inf, np.nan, 0.0
+    sb[1], sb[2], sb[3], sb[4] = -np.inf, np.nan, 0.0, 3e38
+    qa[:, 0], qb[:, 0] = 127, 127                        # fp16 leaves its range in places
+    sb[5:9] = 1e3
+    want = expected(dtype, qa, sa, qb, sb)
+    assert bool(want.isnan().any() and want.isinf().any())
+    assert exactly(run((qa, sa, qb, sb), dtype), want)
+    ua, us, ub, ut = (upload(x) for x in (qa, sa, qb, sb))
+    for expected_m in (1, m):
+        d = torch.full((2, m, n), FILL, dtype=dtype, device=device())
+        dg.m_grouped_int8_gemm_nt_masked((ua.expand(2, m, k).contiguous(), us.expand(2, m).contiguous()),
+                                         (ub.expand(2, n, k).contiguous(), ut.expand(2, n).contiguous()), d,
+                                         torch.tensor([m, m - 1], dtype=torch.int32, device=device()), expected_m)
+        assert exactly(d[0], want) and exactly(d[1, :m - 1], want[:m - 1]) and bool((d[1, m - 1] == FILL).all())
+    rows = (m + 127) // 128 * 128
+    pa, ps = torch.zeros((rows, k), dtype=torch.int8, device=device()), torch.zeros(rows, device=device())
+    pa[:m], ps[:m] = ua, us
+    idx = torch.full((rows,), -1, dtype=torch.int32, device=device())
+    idx[:m] = 0
+    d = torch.full((rows, n), FILL, dtype=dtype, device=device())
+    dg.m_grouped_int8_gemm_nt_contiguous((pa, ps), (ub[None], ut[None]), d, idx)
+    assert exactly(d[:m], want) and bool((d[m:] == FILL).all())

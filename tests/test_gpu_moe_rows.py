@@ -310,3 +310,10 @@ def test_small_layouts_take_no_workspace():
                                               slot_row.data_ptr(), None, 0, stream) == 0
         for got, want in zip((row_slot, slot_row, counts), moe.layout_masked(idx.cpu().numpy(), 60, 16)):
             assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_combine_grad_without_columns():
+    lay = dg.expert_layout_contiguous(torch.from_numpy(routing(5, 2, 3, seed=1)).to(device()), 3)
+    none = torch.empty((lay.rows, 0), dtype=torch.bfloat16, device=device())
+    dy, dw = dg.combine_grad(none[:5], none, lay.slot_row, lay.row_slot, torch.ones((5, 2), device=device()))
+    assert dy.shape == (lay.rows, 0) and bool((dw == 0).all())
