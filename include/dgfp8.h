@@ -524,7 +524,8 @@ dg_status dg_m_grouped_int8_gemm_nt_masked(const void* a, int64_t lda, int64_t a
  *   amax = max |x| over the row;  s = fl32(max(amax, 1e-4) / 127);
  *   q = fl32(x / s) rounded to the nearest whole number, ties to even: -127..127.
  * Bit-exact with this definition.  A row with an infinity or a NaN gets an
- * infinite or NaN scale and unspecified codes: the product's row shows it.
+ * infinite or NaN scale and unspecified codes: the product's row shows it.  The floor of 1e-4
+ * is the FP8 cast's; a row whose maximum lies below it uses fewer than 127 steps.
  *   x   device, dtype (DG_F32 or DG_BF16) [m, k], row stride ldx, rows at 16-byte
  *       boundaries
  *   q   device, int8 [m, k], row stride ldq, rows at 16-byte boundaries
@@ -564,6 +565,9 @@ typedef enum dg_route_score { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 } dg_ro
  * largest key:
  *   w_j = scale * s_j,  or  scale * s_j / (sum of the chosen s)  if renormalize != 0
  * (0 if that sum is 0: every chosen sigmoid underflowed).
+ *   Scores are fp32, within a few units of their last place, and a row's softmax is summed in an
+ * order that depends on tokens, experts and groups.  With a bias or group sums, keys that close
+ * may be ranked differently in calls of different sizes; the same call always gives the same bits.
  *   Unavailable experts: a logit or a bias of -inf takes an expert out.  Where
  * fewer than topk are left, the last slots get index -1 and weight 0 (a row
  * masked whole gets only those).  A NaN logit or bias (and, under softmax, a

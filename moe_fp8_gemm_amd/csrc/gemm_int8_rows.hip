@@ -15,7 +15,8 @@
 // Measured against the best tiled plan, operands in HBM (us): 4096x7168 M = 1: 8.5
 // to 11.1, M = 8: 9.5 to 11.4, M = 16: 10.6 to 11.4; 7168x16384 M = 1: 29.6 to
 // 29.8, M = 8: 32.6 to 29.1, M = 16: 37.6 to 29.1; 2112x7168 M = 8: 8.7 to 9.7; 1024x512 M = 1:
-// 2.8 to 3.8.  Hence up to 8 rows.  2, 4 or 16 waves along K and 2 or 8 pieces ahead
+// 2.8 to 3.8.  Hence up to 8 rows, whatever K: at 16384 deep that loses 12% with all 8 of them, and
+// at 7168 deep another 8 rows would still gain.  2, 4 or 16 waves along K and 2 or 8 pieces ahead
 // came within 5% of this choice or behind it.  The masked rule and its figures stand
 // at run_masked_int8; 32 rows of A at a time lost to 16 at every count up to 16 and
 // to the 64-row tiles beyond.

@@ -34,10 +34,10 @@
 // Where more than kLanes keys reach the bound it is raised by halving; where that
 // does not help (equal keys) the rounds run after all.  Every step is written for all
 // values at once and without branches: a lone wave's time is its chain of
-// instructions at 7 to 8 cycles each.  Measured on 32768 x 256 bf16 logits, top 8: 18.1 us
-// with rounds alone, 9.2 us so (16.8 MB; the vector instructions bound it); with sigmoid
-// scores, a bias and 4 of 8 groups of fp32 logits 18.5 us; one token 3.3 and 4.6 us, an
-// empty launch 2.3.
+// instructions at 7 to 8 cycles each.  Measured on 32768 x 256 bf16 logits, top 8, in a graph
+// that goes through eight inputs: 18.1 us with rounds alone, 9.2 us so (16.8 MB; the vector
+// instructions bound it; 8.4 us where two inputs take turns); with sigmoid scores, a bias and 4
+// of 8 groups of fp32 logits 20 us; one token 2.6 and 3.8 us.
 #include "elem_types.h"
 #include "moe_internal.h"
 
@@ -682,7 +682,8 @@ hipError_t grad_launch(const RouteGradParams& p, hipStream_t stream) {
 // 6.1, 2048 tokens 6.4 to 7.0, 4096 tokens 8.4 to 7.1; bf16 logits alone: 3.3 to 3.7, 4.1 to
 // 4.6, 4.9 to 4.7).  Groups that are no whole runs of 16 experts leave few lanes with keys
 // and so a low bound; four experts a lane find a better one (160 experts in 8 groups,
-// top 6: 1024 tokens 5.8 to 9.5, 8192 tokens 10.5 to 11.3, 16384 tokens 16.8 to 16.0).
+// top 6: 1024 tokens 5.8 to 9.5, 8192 tokens 10.5 to 11.3, 16384 tokens 16.8 to 16.0; measured on
+// these groups only, and taken to hold for the other sizes above 128 experts).
 constexpr int64_t kWaveTokens = 2048, kWaveTokensOddGroups = 8192;
 template <class T>
 hipError_t route_sized(const RouteParams& p, hipStream_t s) {

@@ -19,6 +19,8 @@ Pair = Tuple[torch.Tensor, torch.Tensor]
 def per_token_cast_int8(x: torch.Tensor, q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None) -> Pair:
     """x bf16 or fp32 [m, k] -> (int8 codes [m, k], fp32 scales [m]): s = max(amax, 1e-4) / 127, q = round(x / s).
 
+    Rows whose maximum lies below 1e-4 use fewer than 127 steps.
+
     Codes allocated here have rows that begin at 128-byte lines (a row stride above k where k is no multiple of 128);
     weights laid out once are best kept that way too.
     """

@@ -13,7 +13,8 @@ A layer runs
     m_grouped_fp8_gemm_nt_contiguous(a, b, d, layout.m_indices)
     out = combine(d, layout.slot_row, weights)
 
-and nothing in it reads the routing on the host.
+and nothing in it reads the routing on the host.  The results are plain tensors: autograd records none of the calls,
+and a training step calls ``route_topk_grad`` and ``combine_grad`` itself.
 """
 from __future__ import annotations
 
