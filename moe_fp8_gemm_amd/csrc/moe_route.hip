@@ -448,8 +448,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteParams p) {
       if (lanes >= 8) join(swap_lanes<4>(a), swap_lanes<4>(b));
       if (lanes >= 16) join(swap_lanes<8>(a), swap_lanes<8>(b));
     };
+    // sums are halved: of the same order, and two of the largest numbers stay in fp32's range
     auto put = [&](int g) {
-      gscore[g] = p.group_top2 && b > kRankLow ? value_of(a) + value_of(b) : value_of(a);
+      const float half = 0.5f * value_of(a);
+      gscore[g] = !p.group_top2 ? value_of(a) : b > kRankLow ? half + 0.5f * value_of(b) : half;
     };
     // a group is a run of whole lanes where its size is kVals times a power of two;
     // other sizes go through LDS, where as many lanes as there are share a group's keys

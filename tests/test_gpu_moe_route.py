@@ -307,3 +307,32 @@ def test_gradient_of_a_logit_without_a_score(score, renormalize, t):
     ok = np.isnan(want).any(1)
     bound = G_TOL * 2.5 * np.abs(g.cpu().numpy()).max(1, keepdims=True)
     assert np.all(np.abs(dx - want)[~ok] <= np.broadcast_to(bound, dx.shape)[~ok])
+
+
+# ---------------------------------------------------------------- biases at the ends of fp32
+
+@pytest.mark.parametrize("t", [3, 9000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups", [(24, 4), (160, 8), (256, 8), (640, 20)])
+def test_group_sums_of_the_largest_biases(e, groups, score, t):
+    """The sum of two scores plus biases leaves fp32's range where both biases are the type's lowest or largest
+    number; the groups are still there, in the order of their sums.  (A score beside such a bias rounds away.)"""
+    size, low, high = e // groups, torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    x = draw(t, e, torch.float32, 12)
+    first = torch.arange(size + 2, device=device(), dtype=torch.int32)
+    kw = dict(score=score, num_expert_groups=groups, group_score="top2")
+
+    bias = torch.full((e,), low, device=device())        # every expert at the lowest value: all keys equal
+    idx, w = dg.route_topk(x, size + 2, bias=bias, topk_groups=2, **kw)
+    assert bool((idx == first).all()) and bool((w > 0).all())
+    assert np.allclose(w.sum(1).cpu().numpy(), 1.0, atol=1e-5)
+
+    bias[2 * size:3 * size] = 0.0                        # one group free: its experts, then the lowest of group 0
+    idx, _ = dg.route_topk(x, size + 2, bias=bias, topk_groups=2, **kw)
+    assert bool((idx[:, size:] == first[:2]).all())
+    assert bool((idx[:, :size].sort(1).values == first[:size] + 2 * size).all())
+
+    bias = torch.full((e,), 0.9 * high, device=device())
+    bias[size:2 * size] = high
+    idx, _ = dg.route_topk(x, size, bias=bias, topk_groups=1, **kw)
+    assert bool((idx == first[:size] + size).all())
