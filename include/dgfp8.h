@@ -701,6 +701,173 @@ dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t 
                           int64_t tokens, int topk, int64_t rows, int64_t h, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Around the products of a layer: norm, gated activation, weights' gradients
+ *
+ * What a layer needs besides routing: the norm before it (with the residual's
+ * addition and the cast), the gated activation between its two products (with the
+ * cast, and an 8-bit checkpoint of its input), their gradients, and the gradients of the
+ * weights over each expert's rows, from the 8-bit activations that the forward pass
+ * kept.  Conventions as above: sizes on the host, everything else on the device;
+ * statistics and sums in fp32; rows at 16-byte boundaries; strides in elements.
+ * Codes and scales follow dg_per_token_cast_fp8 and dg_per_token_cast_int8 for
+ * the fp32 values that are cast, except that a NaN shows: a block (int8: a row) that
+ * holds one gets a NaN scale.
+ */
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   h = x + residual, rounded to x's type;
+ *   rstd = (sum h^2 / k + eps)^-1/2;   y = h * rstd * weight, rounded to x's type.
+ * The norm is that of the rounded h, so that h and rstd are all its gradient needs.
+ *   x         device, dtype [rows, k], row stride ldx
+ *   residual  device, dtype [rows, k], row stride ldr, or NULL: h = x
+ *   weight    device, [k] of weight_dtype (dtype or DG_F32), 16-byte aligned, or NULL: ones
+ *   eps       >= 0, finite.  A row of zeros with eps == 0 gives NaN
+ *   h         device, dtype [rows, k], row stride ldh, or NULL: not written
+ *   y         device, dtype [rows, k], row stride ldy
+ *   rstd      device, fp32 [rows], or NULL: not written
+ * h and y may be x or residual (same address and stride), not each other.  An element past
+ * 1.8e19 overflows its square: rstd is 0 then.  A NaN or an infinity makes its row NaN
+ * (where it is finite, 0).
+ * Limits: k % 8 == 0, k <= 16384, rows <= 2^23 -> otherwise DG_ERROR_NOT_SUPPORTED, as for
+ * misaligned rows.
+ */
+dg_status dg_rms_norm(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, int weight_dtype, float eps, void* h, int64_t ldh,
+                      void* y, int64_t ldy, float* rstd, int64_t rows, int64_t k, void* stream);
+
+/* The same with the FP8 cast of y's fp32 values: q E4M3 [rows, k], row stride ldq; sf fp32
+ * [rows, k/128] with strides sf_sm, sf_sk; ue8m0 as in the casts.  k % 128 == 0.
+ * y may be NULL: not written. */
+dg_status dg_rms_norm_cast_fp8(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr,
+                               const void* weight, int weight_dtype, float eps, void* h, int64_t ldh,
+                               void* y, int64_t ldy, float* rstd, void* q, int64_t ldq,
+                               float* sf, int64_t sf_sm, int64_t sf_sk,
+                               int64_t rows, int64_t k, int ue8m0, void* stream);
+
+/* The same with the int8 cast: q int8 [rows, k], sf fp32 [rows] with stride sf_s.
+ * k % 16 == 0. */
+dg_status dg_rms_norm_cast_int8(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr,
+                                const void* weight, int weight_dtype, float eps, void* h, int64_t ldh,
+                                void* y, int64_t ldy, float* rstd, void* q, int64_t ldq,
+                                float* sf, int64_t sf_s, int64_t rows, int64_t k, void* stream);
+
+/*
+ * Gradient of the norm, with n = h * rstd:
+ *   dx = dh + rstd * (weight * dy - n * mean(weight * dy * n)),  rounded to dtype;
+ *   dweight = sum over the rows of dy * n,  fp32.
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h     device, dtype [rows, k]: the gradient of y, and h as the norm wrote it
+ *   rstd      device, fp32 [rows], as the norm wrote it
+ *   dh        device, dtype [rows, k], row stride lddh: the gradient that reaches h by another
+ *             way (the residual stream), or NULL: none
+ *   dx        device, dtype [rows, k], row stride lddx; may be dy, h or dh (same stride)
+ *   dweight   device, fp32 [k], or NULL: not computed.  Overwritten; without rows, zeros
+ *   ws        device, 16-byte aligned, dg_rms_norm_grad_workspace_size() bytes (contents do
+ *             not matter); may be NULL without dweight
+ * Sums are taken in an order that rows and k alone give.  Limits as dg_rms_norm.
+ */
+dg_status dg_rms_norm_grad(const void* dy, int dtype, int64_t lddy, const void* h, int64_t ldh,
+                           const void* weight, int weight_dtype, const float* rstd,
+                           const void* dh, int64_t lddh, void* dx, int64_t lddx, float* dweight,
+                           int64_t rows, int64_t k, void* ws, size_t ws_bytes, void* stream);
+size_t dg_rms_norm_grad_workspace_size(int64_t rows, int64_t k);
+
+/*
+ * Gated activation with the FP8 cast:  a = silu(h[:, :inner]) * h[:, inner:], silu(g) =
+ * g / (1 + e^-g), in fp32 from the stored h, then cast in blocks of 128.
+ *   h         device, dtype [rows, 2 * inner], row stride ldh: gate and up side by side
+ *   m_indices device, int32 [rows], or NULL: rows whose entry is negative are left untouched
+ *             (the contiguous layout's padding)
+ *   masked_m  device, int32 [num_groups], or NULL: rows is num_groups * max_m, and only the first
+ *             masked_m[g] rows of each group's are done (clamped to 0..max_m).  Not both
+ *   q, sf     device, E4M3 [rows, inner], fp32 [rows, inner/128] with strides sf_sm, sf_sk
+ *   hq, hsf   device, E4M3 [rows, 2 * inner], fp32 [rows, 2 * inner / 128]: the FP8 cast of h
+ *             itself, for dg_swiglu_grad; or hq NULL: none
+ * Limits: inner % 128 == 0, inner <= 2^24, rows <= 2^23, num_groups <= 1024.
+ */
+dg_status dg_swiglu_cast_fp8(const void* h, int dtype, int64_t ldh, const int32_t* m_indices,
+                             const int32_t* masked_m, int num_groups, void* q, int64_t ldq,
+                             float* sf, int64_t sf_sm, int64_t sf_sk, void* hq, int64_t ldhq,
+                             float* hsf, int64_t hsf_sm, int64_t hsf_sk,
+                             int64_t rows, int64_t inner, int ue8m0, void* stream);
+
+/* The same with the int8 cast: q int8 [rows, inner], sf fp32 [rows] with stride sf_s.
+ * inner % 16 == 0, inner <= 16384. */
+dg_status dg_swiglu_cast_int8(const void* h, int dtype, int64_t ldh, const int32_t* m_indices,
+                              const int32_t* masked_m, int num_groups, void* q, int64_t ldq,
+                              float* sf, int64_t sf_s, int64_t rows, int64_t inner, void* stream);
+
+/*
+ * Gradient of the gated activation, with g, u the halves of h and s = 1 / (1 + e^-g):
+ *   dh[:, :inner] = da * u * s * (1 + g * (1 - s)),   dh[:, inner:] = da * g * s.
+ *   da        device, dtype [rows, inner], row stride ldda
+ *   h         device, dtype [rows, 2 * inner]; or NULL and
+ *   hq, hsf   the checkpoint that dg_swiglu_cast_fp8 wrote: the gradient at the values that it
+ *             stands for
+ *   m_indices, masked_m as in dg_swiglu_cast_fp8
+ *   dh        device, dtype [rows, 2 * inner], row stride lddh; may be h (same stride)
+ *   q, sf     device, E4M3 [rows, 2 * inner], fp32 [rows, 2 * inner / 128]: the FP8 cast of dh's fp32
+ *             values, for the product that follows; or q NULL: none
+ * inner % 128 == 0 with codes on either side, otherwise inner % 8 == 0; limits as above.
+ */
+dg_status dg_swiglu_grad(const void* da, int dtype, int64_t ldda, const void* h, int64_t ldh,
+                         const void* hq, int64_t ldhq, const float* hsf, int64_t hsf_sm, int64_t hsf_sk,
+                         const int32_t* m_indices, const int32_t* masked_m, int num_groups,
+                         void* dh, int64_t lddh, void* q, int64_t ldq,
+                         float* sf, int64_t sf_sm, int64_t sf_sk,
+                         int64_t rows, int64_t inner, int ue8m0, void* stream);
+
+/*
+ * Gradient of a weight [n, k] of a product y = x . W^T:  dw[n, k] = sum over the rows r of
+ * dy[r, n] * x[r, k].
+ *   dy        device, bf16 [rows, n], row stride lddy
+ *   x         device, [rows, k], row stride ldx: bf16 where sf is NULL; otherwise E4M3 codes with
+ *             scales sf, fp32 [rows, k/128] with strides sf_sm, sf_sk (the operand that the forward
+ *             product read).  A code times its scale enters the product rounded to bf16: exact where
+ *             the scale is a power of two.
+ *   dw        device, out_dtype (DG_F32 or DG_BF16) [n, k], row stride lddw
+ *   accumulate  nonzero: the sum is added to dw (DG_F32 only)
+ *   ws        device, 16-byte aligned, dg_weight_grad_workspace_size() bytes (contents do not
+ *             matter): lets several workgroups share a tile's rows where there are few tiles; NULL
+ *             or smaller: they do not.  Calls that may overlap need distinct ones
+ * Sums are fp32, in an order that the sizes alone give.
+ * Limits: n % 8 == 0, k % 8 == 0 (codes: k % 128 == 0), n, k, lddy, ldx < 2^24, rows < 2^31, rows of
+ * dy, x and dw at 16-byte boundaries -> otherwise DG_ERROR_NOT_SUPPORTED.  rows == 0 gives zeros.
+ */
+dg_status dg_weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                         const float* sf, int64_t sf_sm, int64_t sf_sk,
+                         void* dw, int out_dtype, int64_t lddw, int accumulate,
+                         int64_t rows, int64_t n, int64_t k, void* ws, size_t ws_bytes, void* stream);
+size_t dg_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int num_groups);
+
+/*
+ * The same for each group (expert) of rows: dw [num_groups, n, k] with group stride
+ * dw_group_stride.  Groups follow one another, each from a multiple of `alignment` rows (128:
+ * dg_expert_layout_contiguous; 1: no padding), counts[g] rows of which count; what lies
+ * between them may hold anything.  A group without rows gets zeros (accumulate: nothing).
+ *   counts    device, int32 [num_groups]; negative ones count as 0, and rows past `rows` are
+ *             left out
+ * num_groups <= 1024.
+ */
+dg_status dg_m_grouped_weight_grad_contiguous(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                              const float* sf, int64_t sf_sm, int64_t sf_sk,
+                                              void* dw, int out_dtype, int64_t lddw, int64_t dw_group_stride,
+                                              const int32_t* counts, int num_groups, int64_t alignment,
+                                              int accumulate, int64_t rows, int64_t n, int64_t k,
+                                              void* ws, size_t ws_bytes, void* stream);
+
+/* The same in the masked layout: group g's rows are g * max_m .. g * max_m + masked_m[g] - 1
+ * (masked_m clamped to 0..max_m) of [num_groups * max_m, ...] operands. */
+dg_status dg_m_grouped_weight_grad_masked(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                          const float* sf, int64_t sf_sm, int64_t sf_sk,
+                                          void* dw, int out_dtype, int64_t lddw, int64_t dw_group_stride,
+                                          const int32_t* masked_m, int num_groups, int64_t max_m,
+                                          int accumulate, int64_t n, int64_t k,
+                                          void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Width of the persistent GEMM grid in compute units (default: all CUs of the
  * current device).  Results never depend on it.  num_cus <= 0 restores the
  * default.  (Analog of set_num_sms: page ssnai.com DeepGEMM analysis.)

@@ -5,7 +5,7 @@ device pointers, strides and torch's current HIP stream to the C ABI declared
 in ``include/dgfp8.h`` and raises ``DgError`` on a non-zero status.  All
 arithmetic runs in the HIP kernels of ``libdgfp8.so``; there is no fallback:
 importing this package fails loudly when the library has not been built.  The
-marshalling of the mixture-of-experts and int8 operators is compiled
+marshalling of the mixture-of-experts, layer and int8 operators is compiled
 (``_native.so``).
 
 Tensor conventions (torch): E4M3 operands are ``torch.float8_e4m3fn`` (or
@@ -66,6 +66,26 @@ _SIGNATURES = {
     "dg_combine": ([_p, _i64, _p, _i64, _p, _i64, _p, _i32, _i64, _i64, _i32, _i64, _i64, _p], _i32),
     "dg_combine_grad": ([_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i32, _i64, _i64,
                          _p], _i32),
+    "dg_rms_norm": ([_p, _i32, _i64, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _i64, _p, _i64, _i64, _p], _i32),
+    "dg_rms_norm_cast_fp8": ([_p, _i32, _i64, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64,
+                              _i64, _i64, _i64, _i32, _p], _i32),
+    "dg_rms_norm_cast_int8": ([_p, _i32, _i64, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64,
+                               _i64, _i64, _p], _i32),
+    "dg_rms_norm_grad": ([_p, _i32, _i64, _p, _i64, _p, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _p, _sz, _p],
+                         _i32),
+    "dg_rms_norm_grad_workspace_size": ([_i64, _i64], _sz),
+    "dg_swiglu_cast_fp8": ([_p, _i32, _i64, _p, _p, _i32, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i64, _i64,
+                            _i64, _i32, _p], _i32),
+    "dg_swiglu_cast_int8": ([_p, _i32, _i64, _p, _p, _i32, _p, _i64, _p, _i64, _i64, _i64, _p], _i32),
+    "dg_swiglu_grad": ([_p, _i32, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _p, _p, _i32, _p, _i64, _p, _i64, _p,
+                        _i64, _i64, _i64, _i64, _i32, _p], _i32),
+    "dg_weight_grad": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i32, _i64, _i32, _i64, _i64, _i64, _p, _sz, _p],
+                       _i32),
+    "dg_weight_grad_workspace_size": ([_i64, _i64, _i64, _i32], _sz),
+    "dg_m_grouped_weight_grad_contiguous": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i32, _i64, _i64, _p, _i32, _i64,
+                                             _i32, _i64, _i64, _i64, _p, _sz, _p], _i32),
+    "dg_m_grouped_weight_grad_masked": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i32, _i64, _i64, _p, _i32, _i64,
+                                         _i32, _i64, _i64, _p, _sz, _p], _i32),
     "dg_status_string": ([_i32], ctypes.c_char_p),
     "dg_fp8_gemm_nt": ([_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p, _i64,
                         _i64, _i64, _i64, _p], _i32),
@@ -464,5 +484,8 @@ _native.connect(DgError, _auto_workspace)
 
 from .int8 import (int8_gemm_nt, m_grouped_int8_gemm_nt_contiguous, m_grouped_int8_gemm_nt_masked,  # noqa: E402
                    per_token_cast_int8)
+from .layer import (m_grouped_weight_grad_contiguous, m_grouped_weight_grad_masked, rms_norm,  # noqa: E402
+                    rms_norm_cast_fp8, rms_norm_cast_int8, rms_norm_grad, swiglu_cast_fp8, swiglu_cast_int8,
+                    swiglu_checkpoint_fp8, swiglu_grad, swiglu_grad_cast_fp8, weight_grad)
 from .moe import (ExpertLayout, combine, combine_grad, dispatch_cast_fp8, dispatch_cast_int8,  # noqa: E402
                   expert_layout_contiguous, expert_layout_masked, expert_layout_rows, route_topk, route_topk_grad)

@@ -29,8 +29,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libdgfp8.so")
 NATIVE_PATH = os.path.join(HERE, "_native.so")
-SOURCES = ["api.cpp", "api_moe.cpp", "gemm_fp8.hip", "gemm_int8.hip", "gemm_int8_rows.hip", "cast_fp8.hip",
-           "scratch.hip", "moe_route.hip", "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip"]
+SOURCES = ["api.cpp", "api_moe.cpp", "api_layer.cpp", "gemm_fp8.hip", "gemm_int8.hip", "gemm_int8_rows.hip", "cast_fp8.hip",
+           "scratch.hip", "moe_route.hip", "moe_layout.hip", "moe_dispatch.hip", "moe_combine.hip",
+           "norm.hip", "swiglu.hip", "weight_grad.hip"]
 ARCH = "gfx950"
 
 

@@ -15,10 +15,6 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 23;
 constexpr int64_t kMaxSlots = (int64_t)1 << 30;
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 
-dg_status of(hipError_t err) { return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH; }
-
-int64_t elem_bytes(int dtype) { return dtype == DG_F32 ? 4 : 2; }
-
 // Checks of the two routing calls, besides their own pointers.
 dg_status check_route(int dtype, int64_t ld, int64_t ldi, int64_t ldw, int64_t tokens, int experts, int topk,
                       int score) {
@@ -37,13 +33,6 @@ dg_status check_map(const void* slot_row, int64_t lds, int64_t tokens, int topk,
   if (tokens > 0 && (!slot_row || lds < topk)) return DG_ERROR_INVALID_VALUE;
   if (topk > kMaxTopk || tokens > kMaxTokens || rows > kMaxRows || !strides_ok({lds})) return DG_ERROR_NOT_SUPPORTED;
   if (!aligned(slot_row, 4)) return DG_ERROR_NOT_SUPPORTED;
-  return DG_SUCCESS;
-}
-
-// A matrix whose rows move in 16-byte pieces.
-dg_status check_rows(const void* p, int64_t ld, int64_t cols, int64_t elem) {
-  if (!p || ld < cols) return DG_ERROR_INVALID_VALUE;
-  if (!strides_ok({ld, cols}) || !aligned(p, 16) || (ld * elem) % 16 != 0) return DG_ERROR_NOT_SUPPORTED;
   return DG_SUCCESS;
 }
 

@@ -1,4 +1,4 @@
-// Argument marshalling of the mixture-of-experts and int8 operators for torch, in C++.
+// Argument marshalling of the mixture-of-experts, layer and int8 operators for torch, in C++.
 //
 // A decoding step's calls work for a few microseconds, less than their arguments
 // cost to check and their outputs to allocate from Python (8 to 11 us a call; 3 to
@@ -444,6 +444,316 @@ PyObject* combine_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- norm
+
+// Weight of a norm over rows of x: defined or not; its type is x's or fp32.
+Tensor norm_weight(const Args& a, int i, const Tensor& x) {
+  if (a.none(i)) return Tensor();
+  const Tensor& w = check(a, i, "weight", type_bit(x) | kF32, 1);
+  shape(a, w, "weight", {x.size(1)});
+  return w;
+}
+
+// FP8 codes and scales [rows, k], [rows, k/128]: passed in, or new ones whose scales of one block
+// lie beside each other along the rows, as the GEMM reads them best.
+struct Codes {
+  Tensor q, sf;
+};
+Codes fp8_out(const Args& a, int q, int sf, int64_t rows, int64_t k, const Tensor& like) {
+  return {output(a, q, "q", {rows, k}, at::kFloat8_e4m3fn, kE4M3 | kU8, like),
+          a.none(sf) ? fresh({k / 128, rows}, at::kFloat, like).t() : scales(a, sf, "sf", {rows, k / 128})};
+}
+
+// kind 0: rows, 1: FP8, 2: int8.  (x, weight, residual, eps, [ue8m0, q, sf | q, sf], y, h, rstd)
+template <int kKind>
+PyObject* norm(PyObject* const* args, const char* name, const char* abi) {
+  const Args a{args, name};
+  const Tensor& x = check(a, 0, "x", kF32 | kBF16 | kF16, 2);
+  const On on(x);
+  const int64_t rows = x.size(0), k = x.size(1);
+  const Tensor w = norm_weight(a, 1, x);
+  Tensor r;
+  if (!a.none(2)) {
+    r = check(a, 2, "residual", type_bit(x), 2);
+    shape(a, r, "residual", x.sizes());
+  }
+  const float eps = (float)a.number(3, "eps");
+  constexpr int at = kKind == 1 ? 7 : kKind == 2 ? 6 : 4;   // y, h, rstd
+  Codes c;
+  if (kKind == 1) c = fp8_out(a, 5, 6, rows, k, x);
+  if (kKind == 2) c = {int8_codes(a, 4, rows, k, x), a.none(5) ? fresh({rows}, at::kFloat, x) : scales(a, 5, "sf", {rows})};
+  Tensor y;
+  if (kKind == 0 || !a.none(at)) y = output(a, at, "y", {rows, k}, x.scalar_type(), type_bit(x), x);
+  Tensor h;
+  if (r.defined() || !a.none(at + 1)) h = output(a, at + 1, "h", {rows, k}, x.scalar_type(), type_bit(x), x);
+  Tensor rstd = output(a, at + 2, "rstd", {rows}, at::kFloat, kF32, x);
+  same_device(a, x, {&w, &r, &c.q, &c.sf, &y, &h, &rstd});
+  TORCH_CHECK_VALUE(!y.defined() || !h.defined() || rows == 0 || k == 0 || y.data_ptr() != h.data_ptr(), a.call,
+                    ": y and h must be different tensors");
+  void* const rp = r.defined() ? ptr(r) : nullptr;
+  void* const wp = w.defined() ? ptr(w) : nullptr;
+  void* const hp = h.defined() ? ptr(h) : nullptr;
+  void* const yp = y.defined() ? ptr(y) : nullptr;
+  const int64_t ldr = r.defined() ? ld(r) : 0, ldh = h.defined() ? ld(h) : 0, ldy = y.defined() ? ld(y) : 0;
+  const int wt = w.defined() ? dtype_of(w) : DG_F32;
+  dg_status st;
+  if constexpr (kKind == 0) {
+    st = dg_rms_norm(ptr(x), dtype_of(x), ld(x), rp, ldr, wp, wt, eps, hp, ldh, yp, ldy, ptr<float>(rstd), rows, k,
+                     on.stream);
+  } else if constexpr (kKind == 1) {
+    st = dg_rms_norm_cast_fp8(ptr(x), dtype_of(x), ld(x), rp, ldr, wp, wt, eps, hp, ldh, yp, ldy, ptr<float>(rstd),
+                              ptr(c.q), ld(c.q), ptr<float>(c.sf), c.sf.stride(0), c.sf.stride(1), rows, k, a.truth(4),
+                              on.stream);
+  } else {
+    st = dg_rms_norm_cast_int8(ptr(x), dtype_of(x), ld(x), rp, ldr, wp, wt, eps, hp, ldh, yp, ldy, ptr<float>(rstd),
+                               ptr(c.q), ld(c.q), ptr<float>(c.sf), c.sf.stride(0), rows, k, on.stream);
+  }
+  if (!done(st, abi)) return nullptr;
+  PyObject* hr = h.defined() ? THPVariable_Wrap(h) : Py_NewRef(args[0]);
+  if (kKind == 0) return Py_BuildValue("(NNN)", THPVariable_Wrap(y), hr, THPVariable_Wrap(rstd));
+  return Py_BuildValue("(NNN)", pair(c.q, c.sf), hr, THPVariable_Wrap(rstd));
+}
+
+PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return norm<0>(args, "rms_norm", "dg_rms_norm");
+  END_HANDLE_TH_ERRORS
+}
+PyObject* rms_norm_cast_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return norm<1>(args, "rms_norm_cast_fp8", "dg_rms_norm_cast_fp8");
+  END_HANDLE_TH_ERRORS
+}
+PyObject* rms_norm_cast_int8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return norm<2>(args, "rms_norm_cast_int8", "dg_rms_norm_cast_int8");
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* rms_norm_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Args a{args, "rms_norm_grad"};
+  const Tensor& dy = check(a, 0, "dy", kF32 | kBF16 | kF16, 2);
+  const On on(dy);
+  const int64_t rows = dy.size(0), k = dy.size(1);
+  const Tensor& h = check(a, 1, "h", type_bit(dy), 2);
+  shape(a, h, "h", {rows, k});
+  const Tensor w = norm_weight(a, 2, dy);
+  const Tensor& rstd = check(a, 3, "rstd", kF32, 1);
+  shape(a, rstd, "rstd", {rows});
+  Tensor dh;
+  if (!a.none(4)) {
+    dh = check(a, 4, "dh", type_bit(dy), 2);
+    shape(a, dh, "dh", {rows, k});
+  }
+  Tensor dx = output(a, 5, "dx", {rows, k}, dy.scalar_type(), type_bit(dy), dy);
+  Tensor dw;
+  if (w.defined()) dw = output(a, 6, "dweight", {k}, at::kFloat, kF32, dy);
+  TORCH_CHECK_VALUE(w.defined() || a.none(6), a.call, ": dweight needs a weight");
+  same_device(a, dy, {&h, &w, &rstd, &dh, &dx, &dw});
+  const size_t need = dw.defined() ? dg_rms_norm_grad_workspace_size(rows, k) : 0;
+  Tensor ws = need ? fresh({(int64_t)need}, at::kByte, dy) : Tensor();
+  if (!done(dg_rms_norm_grad(ptr(dy), dtype_of(dy), ld(dy), ptr(h), ld(h), w.defined() ? ptr(w) : nullptr,
+                             w.defined() ? dtype_of(w) : DG_F32, f32(rstd), dh.defined() ? ptr(dh) : nullptr,
+                             dh.defined() ? ld(dh) : 0, ptr(dx), ld(dx), dw.defined() ? ptr<float>(dw) : nullptr, rows, k,
+                             need ? ptr(ws) : nullptr, need, on.stream),
+            "dg_rms_norm_grad"))
+    return nullptr;
+  return Py_BuildValue("(NN)", THPVariable_Wrap(dx), dw.defined() ? THPVariable_Wrap(dw) : Py_NewRef(Py_None));
+  END_HANDLE_TH_ERRORS
+}
+
+// ---- gated activation
+
+// Rows of a layout: (m_indices or None, masked_m or None).
+struct Where {
+  Tensor m_indices, masked_m;
+  const int32_t* mi = nullptr;
+  const int32_t* mm = nullptr;
+  int groups = 0;
+};
+Where rows_of(const Args& a, int i, int64_t rows) {
+  Where w;
+  TORCH_CHECK_VALUE(a.none(i) || a.none(i + 1), a.call, ": m_indices and masked_m cannot both be given");
+  if (!a.none(i)) {
+    w.m_indices = check(a, i, "m_indices", kI32, 1);
+    shape(a, w.m_indices, "m_indices", {rows});
+    w.mi = i32(w.m_indices);
+  }
+  if (!a.none(i + 1)) {
+    w.masked_m = check(a, i + 1, "masked_m", kI32, 1);
+    const int64_t g = w.masked_m.size(0);
+    TORCH_CHECK_VALUE(g > 0 && g <= INT32_MAX && rows % g == 0, a.call, ": ", rows, " rows are no multiple of ", g,
+                      " groups");
+    w.groups = (int)g;
+    w.mm = i32(w.masked_m);
+  }
+  return w;
+}
+
+int64_t inner_of(const Args& a, const Tensor& h) {
+  TORCH_CHECK_VALUE(h.size(1) % 2 == 0, a.call, ": h must have an even number of columns, got ", h.size(1));
+  return h.size(1) / 2;
+}
+
+// (h, m_indices, masked_m, ue8m0, q, sf[, hq, hsf])
+PyObject* swiglu_fp8(PyObject* const* args, const char* name, bool keep) {
+  const Args a{args, name};
+  const Tensor& h = check(a, 0, "h", kF32 | kBF16 | kF16, 2);
+  const On on(h);
+  const int64_t rows = h.size(0), inner = inner_of(a, h);
+  const Where w = rows_of(a, 1, rows);
+  const Codes c = fp8_out(a, 4, 5, rows, inner, h);
+  Codes kept;
+  if (keep) kept = fp8_out(a, 6, 7, rows, 2 * inner, h);
+  same_device(a, h, {&w.m_indices, &w.masked_m, &c.q, &c.sf, &kept.q, &kept.sf});
+  if (!done(dg_swiglu_cast_fp8(ptr(h), dtype_of(h), ld(h), w.mi, w.mm, w.groups, ptr(c.q), ld(c.q), ptr<float>(c.sf),
+                               c.sf.stride(0), c.sf.stride(1), keep ? ptr(kept.q) : nullptr, keep ? ld(kept.q) : 0,
+                               keep ? ptr<float>(kept.sf) : nullptr, keep ? kept.sf.stride(0) : 0,
+                               keep ? kept.sf.stride(1) : 0, rows, inner, a.truth(3), on.stream),
+            "dg_swiglu_cast_fp8"))
+    return nullptr;
+  return keep ? Py_BuildValue("(NN)", pair(c.q, c.sf), pair(kept.q, kept.sf)) : pair(c.q, c.sf);
+}
+
+PyObject* swiglu_cast_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return swiglu_fp8(args, "swiglu_cast_fp8", false);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* swiglu_checkpoint_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return swiglu_fp8(args, "swiglu_checkpoint_fp8", true);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* swiglu_cast_int8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  const Args a{args, "swiglu_cast_int8"};
+  const Tensor& h = check(a, 0, "h", kF32 | kBF16 | kF16, 2);
+  const On on(h);
+  const int64_t rows = h.size(0), inner = inner_of(a, h);
+  const Where w = rows_of(a, 1, rows);
+  Tensor q = int8_codes(a, 3, rows, inner, h);
+  Tensor sf = a.none(4) ? fresh({rows}, at::kFloat, h) : scales(a, 4, "sf", {rows});
+  same_device(a, h, {&w.m_indices, &w.masked_m, &q, &sf});
+  if (!done(dg_swiglu_cast_int8(ptr(h), dtype_of(h), ld(h), w.mi, w.mm, w.groups, ptr(q), ld(q), ptr<float>(sf),
+                                sf.stride(0), rows, inner, on.stream),
+            "dg_swiglu_cast_int8"))
+    return nullptr;
+  return pair(q, sf);
+  END_HANDLE_TH_ERRORS
+}
+
+// (da, h, hq, hsf, m_indices, masked_m, [ue8m0,] dh[, q, sf]): h, or its checkpoint (hq, hsf)
+PyObject* swiglu_back(PyObject* const* args, const char* name, bool cast) {
+  const Args a{args, name};
+  const Tensor& da = check(a, 0, "da", kF32 | kBF16 | kF16, 2);
+  const On on(da);
+  const int64_t rows = da.size(0), inner = da.size(1);
+  Tensor h, hq, hsf;
+  if (!a.none(1)) {
+    h = check(a, 1, "h", type_bit(da), 2);
+    shape(a, h, "h", {rows, 2 * inner});
+  } else {
+    hq = check(a, 2, "h's codes", kE4M3 | kU8, 2);
+    shape(a, hq, "h's codes", {rows, 2 * inner});
+    hsf = scales(a, 3, "h's scales", {rows, 2 * inner / 128});
+  }
+  const Where w = rows_of(a, 4, rows);
+  Tensor dh = output(a, cast ? 7 : 6, "dh", {rows, 2 * inner}, da.scalar_type(), type_bit(da), da);
+  Codes c;
+  if (cast) c = fp8_out(a, 8, 9, rows, 2 * inner, da);
+  same_device(a, da, {&h, &hq, &hsf, &w.m_indices, &w.masked_m, &dh, &c.q, &c.sf});
+  const bool codes = hq.defined();
+  if (!done(dg_swiglu_grad(ptr(da), dtype_of(da), ld(da), codes ? nullptr : ptr(h), codes ? 0 : ld(h),
+                           codes ? ptr(hq) : nullptr, codes ? ld(hq) : 0, codes ? f32(hsf) : nullptr,
+                           codes ? hsf.stride(0) : 0, codes ? hsf.stride(1) : 0, w.mi, w.mm, w.groups, ptr(dh), ld(dh),
+                           cast ? ptr(c.q) : nullptr, cast ? ld(c.q) : 0, cast ? ptr<float>(c.sf) : nullptr,
+                           cast ? c.sf.stride(0) : 0, cast ? c.sf.stride(1) : 0, rows, inner, cast && a.truth(6),
+                           on.stream),
+            "dg_swiglu_grad"))
+    return nullptr;
+  return cast ? Py_BuildValue("(NN)", THPVariable_Wrap(dh), pair(c.q, c.sf)) : THPVariable_Wrap(dh);
+}
+
+PyObject* swiglu_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return swiglu_back(args, "swiglu_grad", false);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* swiglu_grad_cast_fp8(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return swiglu_back(args, "swiglu_grad_cast_fp8", true);
+  END_HANDLE_TH_ERRORS
+}
+
+// ---- weights' gradients: (dy, x, sf or None, dw, ...)
+
+enum Grouping { kDense, kContiguous, kMasked };
+
+PyObject* weights_gradient(PyObject* const* args, const char* name, const char* abi, Grouping how) {
+  const Args a{args, name};
+  const Tensor& dy = check(a, 0, "dy", kBF16, 2);
+  const On on(dy);
+  const bool codes = !a.none(2);
+  const Tensor& x = check(a, 1, "x", codes ? kE4M3 | kU8 : kBF16, 2);
+  const int64_t rows = dy.size(0), n = dy.size(1), k = x.size(1);
+  shape(a, x, "x", {rows, k});
+  Tensor sf, counts;
+  if (codes) sf = scales(a, 2, "x's scales", {rows, k / 128});
+  const int64_t dim = how == kDense ? 2 : 3;
+  const Tensor& dw = check(a, 3, "dw", kF32 | kBF16, dim);
+  int64_t groups = 1;
+  if (how == kDense) {
+    shape(a, dw, "dw", {n, k});
+  } else {
+    counts = check(a, 4, how == kMasked ? "masked_m" : "counts", kI32, 1);
+    groups = counts.size(0);
+    shape(a, dw, "dw", {groups, n, k});
+    TORCH_CHECK_VALUE(groups <= INT32_MAX, a.call, ": too many groups");
+    TORCH_CHECK_VALUE(how == kContiguous || (groups > 0 ? rows % groups == 0 : rows == 0), a.call, ": ", rows,
+                      " rows are no multiple of ", groups, " groups");
+  }
+  same_device(a, dy, {&x, &sf, &dw, &counts});
+  const size_t need = dg_weight_grad_workspace_size(rows, n, k, (int)groups);
+  Tensor ws = need ? fresh({(int64_t)need}, at::kByte, dy) : Tensor();
+  void* const wp = need ? ptr(ws) : nullptr;
+  const float* const sp = codes ? f32(sf) : nullptr;
+  const int64_t s0 = codes ? sf.stride(0) : 0, s1 = codes ? sf.stride(1) : 0;
+  dg_status st;
+  if (how == kDense) {
+    st = dg_weight_grad(ptr(dy), ld(dy), ptr(x), ld(x), sp, s0, s1, ptr(dw), dtype_of(dw), ld(dw), a.truth(4), rows, n,
+                        k, wp, need, on.stream);
+  } else if (how == kContiguous) {
+    st = dg_m_grouped_weight_grad_contiguous(ptr(dy), ld(dy), ptr(x), ld(x), sp, s0, s1, ptr(dw), dtype_of(dw),
+                                             ld(dw, 1), dw.stride(0), i32(counts), (int)groups,
+                                             a.integer(5, "alignment"), a.truth(6), rows, n, k, wp, need, on.stream);
+  } else {
+    st = dg_m_grouped_weight_grad_masked(ptr(dy), ld(dy), ptr(x), ld(x), sp, s0, s1, ptr(dw), dtype_of(dw), ld(dw, 1),
+                                         dw.stride(0), i32(counts), (int)groups, groups > 0 ? rows / groups : 0,
+                                         a.truth(5), n, k, wp, need, on.stream);
+  }
+  if (!done(st, abi)) return nullptr;
+  return Py_NewRef(args[3]);
+}
+
+PyObject* weight_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return weights_gradient(args, "weight_grad", "dg_weight_grad", kDense);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* weight_grad_contiguous(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return weights_gradient(args, "m_grouped_weight_grad_contiguous", "dg_m_grouped_weight_grad_contiguous", kContiguous);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* weight_grad_masked(PyObject*, PyObject* const* args, Py_ssize_t) {
+  HANDLE_TH_ERRORS
+  return weights_gradient(args, "m_grouped_weight_grad_masked", "dg_m_grouped_weight_grad_masked", kMasked);
+  END_HANDLE_TH_ERRORS
+}
+
 // ---- int8 products: (qa, sa, qb, sb, d, ...)
 
 PyObject* int8_gemm_nt(PyObject*, PyObject* const* args, Py_ssize_t) {
@@ -552,6 +862,18 @@ PyMethodDef methods[] = {
     DG_METHOD(per_token_cast_int8, 3),
     DG_METHOD(combine, 4),
     DG_METHOD(combine_grad, 7),
+    DG_METHOD(rms_norm, 7),
+    DG_METHOD(rms_norm_cast_fp8, 10),
+    DG_METHOD(rms_norm_cast_int8, 9),
+    DG_METHOD(rms_norm_grad, 7),
+    DG_METHOD(swiglu_cast_fp8, 6),
+    DG_METHOD(swiglu_checkpoint_fp8, 8),
+    DG_METHOD(swiglu_cast_int8, 5),
+    DG_METHOD(swiglu_grad, 7),
+    DG_METHOD(swiglu_grad_cast_fp8, 10),
+    DG_METHOD(weight_grad, 5),
+    DG_METHOD(weight_grad_contiguous, 7),
+    DG_METHOD(weight_grad_masked, 6),
     DG_METHOD(int8_gemm_nt, 6),
     DG_METHOD(int8_contiguous, 7),
     DG_METHOD(int8_masked, 7),

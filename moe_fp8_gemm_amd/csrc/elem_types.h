@@ -1,4 +1,4 @@
-// Element types of the mixture-of-experts kernels and their conversions.
+// Element types of the kernels that move rows, and their conversions.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -61,24 +61,28 @@ __device__ __forceinline__ void widen_eight(const Eight<T>& v, float (&x)[8]) {
     }
   }
 }
-// Stores pass through as well: the rows moved here exceed L2 many times over.
 template <class T>
-__device__ __forceinline__ void store_eight(typename T::store* dst, const float (&x)[8]) {
+__device__ __forceinline__ Eight<T> narrow_eight(const float (&x)[8]) {
+  Eight<T> v;
   if constexpr (sizeof(typename T::store) == 4) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(x[4 * h + i]);
-      __builtin_nontemporal_store(v, (u32x4*)dst + h);
-    }
+    for (int i = 0; i < 8; ++i) v.q[i / 4][i % 4] = __float_as_uint(x[i]);
   } else {
-    u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = (uint32_t)narrow(T{}, x[2 * i]) | ((uint32_t)narrow(T{}, x[2 * i + 1]) << 16);
-    __builtin_nontemporal_store(v, (u32x4*)dst);
+      v.q[0][i] = (uint32_t)narrow(T{}, x[2 * i]) | ((uint32_t)narrow(T{}, x[2 * i + 1]) << 16);
   }
+  return v;
+}
+// Stores pass through as well: the rows moved here exceed L2 many times over.
+template <class T>
+__device__ __forceinline__ void stream_out(typename T::store* dst, const Eight<T>& v) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(typename T::store) / 2); ++i) __builtin_nontemporal_store(v.q[i], (u32x4*)dst + i);
+}
+template <class T>
+__device__ __forceinline__ void store_eight(typename T::store* dst, const float (&x)[8]) {
+  stream_out<T>(dst, narrow_eight<T>(x));
 }
 
 // LDS written by one lane and read by another lane of the same wave.

@@ -9,52 +9,14 @@
 //
 // Bound by memory: tokens x k elements read, rows x k codes written.  Nothing is
 // read twice, and the copies leave as whole 16-byte pieces, 1 KB a wave.
+#include "cast_rules.h"
 #include "elem_types.h"
 #include "moe_internal.h"
 
 namespace dgfp8 {
 namespace {
 
-constexpr float kE4M3Max = 448.0f;
-constexpr float kInt8Max = 127.0f;
-constexpr float kAmaxFloor = 1e-4f;
 constexpr int kThreads = 256;
-
-// |x| as bits: of the same order for whole numbers, and a NaN is the largest.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// Correctly rounded fl32(x / s) for a normal positive s from y = fl32(1 / s): the
-// quotient |x| y is within an ulp, its remainder is exact in one FMA and corrects
-// it.  Quotients too small for that to hold are far below half a code.
-struct Divisor {
-  float s, y;
-};
-__device__ __forceinline__ float divide(float x, Divisor d) {
-#pragma clang fp contract(off)
-  const float q = x * d.y;
-  const float rem = __builtin_fmaf(-q, d.s, x);
-  return __builtin_fmaf(rem, d.y, q);
-}
-
-__device__ __forceinline__ float fp8_scale(uint32_t amax, int ue8m0) {
-  float s = fmaxf(__uint_as_float(amax), kAmaxFloor) / kE4M3Max;
-  if (ue8m0) {
-    uint32_t u = __float_as_uint(s);
-    if (u & 0x007FFFFFu) u = (u & 0x7F800000u) + 0x00800000u;
-    s = __uint_as_float(u);
-  }
-  return s;
-}
-
-__device__ __forceinline__ uint32_t fp8_of_four(const float* x, Divisor d) {
-  float t[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    t[i] = __builtin_copysignf(fminf(divide(fabsf(x[i]), d), kE4M3Max), x[i]);
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-  v = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
-  return (uint32_t)v;
-}
 
 // Token of a workgroup.  Workgroup b runs on XCD b % 8; a run of neighbouring
 // tokens goes to each XCD, because neighbouring tokens fill neighbouring rows of an
@@ -140,29 +102,12 @@ __global__ void __launch_bounds__(kThreads) cast_int8_kernel(DispatchParams p) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) amax = max(amax, wave_max[w]);
-  // A row with a NaN gets a NaN scale (and an infinite one an infinite scale): the
-  // product's row shows it.
-  const float s = amax > 0x7F800000u ? __builtin_nanf("") : fmaxf(__uint_as_float(amax), kAmaxFloor) / kInt8Max;
+  const float s = int8_scale(amax);
   const Divisor d{s, 1.0f / s};
   auto code_of = [&](const Eight<T>& v) -> u32x2 {
     float x[8];
     widen_eight(v, x);
-    uint32_t whole[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = fminf(fmaxf(divide(x[i], d), -kInt8Max), kInt8Max);   // NaN -> -127: any finite code
-      // at 1.5 * 2^23 fp32 holds whole numbers: the sum is q rounded to nearest even, its low
-      // byte the code
-      whole[i] = __float_as_uint(q + 0x1.8p23f);
-    }
-    u32x2 c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __builtin_amdgcn_perm(whole[4 * h + 1], whole[4 * h], 0x0C0C0400);
-      const uint32_t hi = __builtin_amdgcn_perm(whole[4 * h + 3], whole[4 * h + 2], 0x0C0C0400);
-      c[h] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
-    }
-    return c;
+    return int8_of_eight(x, d);
   };
   const int copies = kScatter ? p.topk : 1;
   const int32_t* rows = kScatter ? p.slot_row + t * p.lds : nullptr;

@@ -15,6 +15,7 @@ Modules:
   decode exactly, scale per K block, accumulate in float64, round once.
 * ``exact`` -- the same GEMM in exact rational arithmetic, for tiny shapes.
 * ``int8``  -- int8 cast per row, and the product with scales per row of either operand.
+* ``layer`` -- norm, gated activation, weights' gradients.
 * ``moe``   -- routing and its gradient, expert layouts, combination and its gradient.
 * ``ue8m0`` -- packing of exponent-only scales, four per int32 word.
 
@@ -26,4 +27,4 @@ the quotient, a skipped fp32 rounding, ties away from zero, UE8M0 rounded down,
 no amax floor, bf16 truncation or double rounding, K-block scale order, the B
 scale index, a spurious factor, a dropped K block) and checks that a pin fails.
 """
-from . import bf16, e4m3, exact, gemm, int8, moe, quant, ue8m0  # noqa: F401
+from . import bf16, e4m3, exact, gemm, int8, layer, moe, quant, ue8m0  # noqa: F401
