@@ -15,7 +15,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 23;         // a workgroup per row: grid x block inside 32 bits
 constexpr int64_t kMaxInner = (int64_t)1 << 24;
 constexpr int64_t kMaxInnerInt8 = 16384;               // a row's results in registers
-constexpr int64_t kMaxLd = ((int64_t)1 << 24) - 1;     // weights' gradients: 64 rows inside 2^31 bytes
+constexpr int64_t kMaxLd = ((int64_t)1 << 24) - 1;     // weights' gradients: 32 rows inside 2^31 bytes
 
 bool is_dtype(int dtype) { return dtype == DG_F32 || dtype == DG_BF16 || dtype == DG_F16; }
 
@@ -96,7 +96,7 @@ dg_status weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
     if ((st = check_rows(dy, lddy, n, 2)) != DG_SUCCESS) return st;
     if ((st = check_rows(x, ldx, k, sf ? 1 : 2)) != DG_SUCCESS) return st;
     if (sf && (st = check_scales(sf, sf_sm, sf_sk)) != DG_SUCCESS) return st;
-    if (lddy > kMaxLd || ldx > kMaxLd) return DG_ERROR_NOT_SUPPORTED;
+    if (lddy > kMaxLd || ldx > kMaxLd || (sf && sf_sm > kMaxLd)) return DG_ERROR_NOT_SUPPORTED;
   }
   if (n % 8 != 0 || k % (sf ? 128 : 8) != 0 || n > kMaxLd || k > kMaxLd) return DG_ERROR_NOT_SUPPORTED;
   if (rows >= (int64_t)1 << 31 || groups > kMaxGroups || !aligned(counts, 4)) return DG_ERROR_NOT_SUPPORTED;
