@@ -13,9 +13,9 @@
 // are stored with their 16- or 32-byte units permuted by the row's number, so that the rows that half a wave
 // reads lie in different banks.
 //
-// Pipeline.  All stages of LDS are in flight; a step multiplies the fragments of one stage, held in
+// Pipeline.  All other stages of LDS are in flight; a step multiplies the fragments of one stage, held in
 // registers, while it reads those of the next into the registers that it has just used (codes are converted on the
-// way), and a barrier after the step's first products hands the buffer of the stage before to the loads.
+// way), and a barrier every step or every other hands the buffers of the stages before to the loads.
 #include "dgfp8_device.h"
 #include "layer_internal.h"
 
@@ -35,15 +35,26 @@ struct Config {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kWaves = kWavesN * kWavesK, kThreads = kWaves * 64;
   static constexpr int kFragN = kTn / kWavesN / 16, kFragK = kTk / kWavesK / 16;
+  // with four stages or fewer a barrier every step keeps more loads on their way than one every other step
+  static constexpr bool kPairs = kStages > 4;
   static constexpr int kPitchN = kTn * 2, kPitchK = kTk * (kFp8 ? 1 : 2);   // bytes of an LDS row
   static constexpr int kBytesN = kStep * kPitchN, kBytesK = kStep * kPitchK;
   static constexpr int kBlocks = kTk / 128;
   static constexpr int kScaleBytes = kFp8 ? kBlocks * kStep * 4 : 0;
   static constexpr int kStageBytes = kBytesN + kBytesK + kScaleBytes;
-  // direct loads of a wave in a stage: two of dy, and of x two, or one of codes and one of scales
-  static constexpr int kLoads = 4;
-  static_assert(kBytesN == kWaves * 2048 && kBytesK == kWaves * (kFp8 ? 1024 : 2048), "a wave's share of a stage");
+  // direct loads of a wave in a stage: of dy and of x, and the rows of each; the first kBlocks waves load a block's
+  // scales too, which the counts that they wait for leave out (they wait a little longer)
+  static constexpr int kLoadsN = kBytesN / 1024 / kWaves, kLoadsK = kBytesK / 1024 / kWaves;
+  static constexpr int kLoads = kLoadsN + kLoadsK;
+  static constexpr int kRowsN = 1024 / kPitchN, kRowsK = 1024 / kPitchK;
+  static_assert(kLoadsN * kWaves * 1024 == kBytesN && kLoadsK * kWaves * 1024 == kBytesK, "a wave's share of a stage");
   static_assert(kFragN >= 2 && kTk / kWavesK <= 128, "a wave's columns lie in one block of scales");
+  // First row of a wave's load.  The rows of one lane in all its loads have the same order of units
+  // (turn16 below), so that its column is the same in each.
+  static constexpr __device__ int row_n(int wave, int load) { return load * 16 + wave * kRowsN; }
+  static constexpr __device__ int row_k(int wave, int load) { return load * 16 + wave * kRowsK; }
+  static_assert(kLoadsN * 16 == kStep, "rows of dy's loads");
+  static_assert(kFp8 ? kLoadsK == 1 : kLoadsK * 16 == kStep, "rows of x's loads");
 };
 
 // Order of a row's units in LDS.  32-byte units of 16-bit rows: half a wave reads rows 0-3 and 8-11 (or 4-7 and
@@ -123,11 +134,20 @@ __global__ void __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[C::kStages * C::kStageBytes];
   __shared__ int32_t group_first[kMaxGroups], group_count[kMaxGroups];
+  __shared__ int16_t group_order[kMaxGroups];
   DG_LAS uint8_t* const base = (DG_LAS uint8_t*)lds;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / C::kWavesK, wk = wave % C::kWavesK;
   if (wave == 0) segments(p, lane, (DG_LAS int32_t*)group_first, (DG_LAS int32_t*)group_count);
+  __syncthreads();
+  // groups with the most rows first: what is left for the last round is short
+  for (int g = threadIdx.x; g < p.groups; g += C::kThreads) {
+    const int32_t c = group_count[g];
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) rank += group_count[h] > c || (group_count[h] == c && h < g);
+    group_order[rank] = (int16_t)g;
+  }
   __syncthreads();
 
   const int tiles_n = (int)((p.n + C::kTn - 1) / C::kTn), tiles_k = (int)((p.k + C::kTk - 1) / C::kTk);
@@ -139,8 +159,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     Unit w;
     // divisions are vector instructions: their results go back to scalar registers
     const int gs = uniform(u / tiles), t = u - gs * tiles;
-    w.g = uniform(gs / p.splits);
-    w.split = gs - w.g * p.splits;
+    const int turn = uniform(gs / p.splits);
+    w.g = uniform(((DG_LAS int16_t*)group_order)[turn]);
+    w.split = gs - turn * p.splits;
     const int band = uniform(t / (4 * tiles_k)), in = t - band * 4 * tiles_k;
     const int high = tiles_n - band * 4 < 4 ? tiles_n - band * 4 : 4;
     const int across = uniform(in / high);
@@ -157,30 +178,24 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
   };
 
   // ---- direct loads: this lane's piece of each
-  constexpr int kRowsN = 1024 / C::kPitchN, kRowsK = 1024 / C::kPitchK;   // rows of a wave's load
   const uint32_t ldn = (uint32_t)(p.lddy * 2), ldk = (uint32_t)(p.ldx * (C::kFp8 ? 1 : 2));   // bytes
-  uint32_t off_n[2], off_k[2];
-  {
-    const int r = wave * kRowsN + lane / (64 / kRowsN), slot = lane % (64 / kRowsN);
-    const uint32_t col = (uint32_t)(((((slot >> 1) ^ turn16(r)) << 1) | (slot & 1)) * 16);
-    off_n[0] = (uint32_t)r * ldn + col;
-    off_n[1] = off_n[0] + 16 * ldn;
+  uint32_t off_n[C::kLoadsN], off_k[C::kLoadsK];
+  auto column16 = [&](int row, int slot) {   // byte of the 16 that belong in this slot of the row
+    return (uint32_t)((((slot >> 1) ^ turn16(row)) << 1) | (slot & 1)) * 16;
+  };
+#pragma unroll
+  for (int j = 0; j < C::kLoadsN; ++j) {
+    constexpr int kSlots = 64 / C::kRowsN;
+    const int r = C::row_n(wave, j) + lane / kSlots;
+    off_n[j] = (uint32_t)r * ldn + column16(r, lane % kSlots);
   }
-  {
-    const int r = wave * kRowsK + lane / (64 / kRowsK), slot = lane % (64 / kRowsK);
-    if constexpr (C::kFp8) {
-      off_k[0] = (uint32_t)r * ldk + (uint32_t)(slot ^ turn8<C::kPitchK>(r)) * 16;
-      off_k[1] = 0;
-    } else {
-      off_k[0] = (uint32_t)r * ldk + (uint32_t)(((((slot >> 1) ^ turn16(r)) << 1) | (slot & 1)) * 16);
-      off_k[1] = off_k[0] + 16 * ldk;
-    }
+#pragma unroll
+  for (int j = 0; j < C::kLoadsK; ++j) {
+    constexpr int kSlots = 64 / C::kRowsK;
+    const int r = C::row_k(wave, j) + lane / kSlots, slot = lane % kSlots;
+    off_k[j] = (uint32_t)r * ldk + (C::kFp8 ? (uint32_t)(slot ^ turn8<C::kPitchK>(r)) * 16 : column16(r, slot));
   }
-  // scales: 8 rows of one block by 8 lanes of each wave
-  constexpr int kScaleRows = kStep * C::kBlocks / C::kWaves;
-  static_assert(!C::kFp8 || kScaleRows == 8, "8 scales a wave");
-  const int scale_row = wave * kScaleRows % kStep, scale_block = wave * kScaleRows / kStep;
-  const uint32_t off_s = C::kFp8 ? (uint32_t)(scale_row + lane) * (uint32_t)(p.sf_s0 * 4) : 0;
+  const uint32_t off_s = C::kFp8 ? (uint32_t)lane * (uint32_t)(p.sf_s0 * 4) : 0;   // lanes 0 .. 31: a block's rows
 
   // where the next stage comes from
   uint64_t src_n = 0, src_k = 0, src_s = 0;
@@ -193,34 +208,45 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     cols_n = (uint32_t)(p.n - w.n0) * 2;
     cols_k = (uint32_t)(p.k - w.k0) * (C::kFp8 ? 1 : 2);
     if constexpr (C::kFp8) {
-      const int64_t block = w.k0 / 128 + scale_block;
+      const int64_t block = w.k0 / 128 + (wave < C::kBlocks ? wave : 0);
       block_in = block * 128 < p.k;
       src_s = (uint64_t)(uintptr_t)p.sf + (uint64_t)(w.row * p.sf_s0 + block * p.sf_s1) * 4;
     }
     src_left = w.left;
   };
-  auto load_stage = [&](int buffer) {
-    const uint32_t at = lds_addr(base) + (uint32_t)buffer * C::kStageBytes;
+  // A stage's loads one by one: what they need first, then each.
+  struct Loads {
+    Rsrc n, k, s;
+    uint32_t at;
+  };
+  auto next_loads = [&](int buffer) -> Loads {
     const uint32_t rows = src_left > kStep ? kStep : src_left < 0 ? 0 : src_left;
-    const Rsrc rn = rsrc_of(src_n, rows ? (rows - 1) * ldn + cols_n : 0);
-    const Rsrc rk = rsrc_of(src_k, rows ? (rows - 1) * ldk + cols_k : 0);
-    const uint32_t at_n = at + (uint32_t)(wave * kRowsN) * C::kPitchN;
-    load16_lds(rn, off_n[0], at_n);
-    load16_lds(rn, off_n[1], at_n + 16 * C::kPitchN);
-    const uint32_t at_k = at + C::kBytesN + (uint32_t)(wave * kRowsK) * C::kPitchK;
-    load16_lds(rk, off_k[0], at_k);
-    if constexpr (C::kFp8) {
-      const uint32_t s0 = (uint32_t)(p.sf_s0 * 4);
-      const Rsrc rs = rsrc_of(src_s, rows && block_in ? (rows - 1) * s0 + 4 : 0);
-      const uint32_t at_s = at + C::kBytesN + C::kBytesK + (uint32_t)(scale_block * kStep + scale_row) * 4;
-      if (lane < kScaleRows) load4_lds(rs, off_s, at_s);
-      src_s += (uint64_t)kStep * s0;
-    } else {
-      load16_lds(rk, off_k[1], at_k + 16 * C::kPitchK);
-    }
+    const uint32_t s0 = C::kFp8 ? (uint32_t)(p.sf_s0 * 4) : 0;
+    Loads l;
+    l.at = lds_addr(base) + (uint32_t)buffer * C::kStageBytes;
+    l.n = rsrc_of(src_n, rows ? (rows - 1) * ldn + cols_n : 0);
+    l.k = rsrc_of(src_k, rows ? (rows - 1) * ldk + cols_k : 0);
+    if constexpr (C::kFp8) l.s = rsrc_of(src_s, rows && block_in ? (rows - 1) * s0 + 4 : 0);
     src_n += (uint64_t)kStep * ldn;
     src_k += (uint64_t)kStep * ldk;
+    src_s += (uint64_t)kStep * s0;
     src_left -= kStep;
+    return l;
+  };
+  auto load_piece = [&](const Loads& l, int i) {
+    if (i < C::kLoadsN) {
+      load16_lds(l.n, off_n[i < C::kLoadsN ? i : 0], l.at + (uint32_t)C::row_n(wave, i) * C::kPitchN);
+    } else if (i < C::kLoadsN + C::kLoadsK) {
+      const int j = i - C::kLoadsN;
+      load16_lds(l.k, off_k[j < C::kLoadsK ? j : 0], l.at + C::kBytesN + (uint32_t)C::row_k(wave, j) * C::kPitchK);
+    } else if (C::kFp8 && wave < C::kBlocks) {
+      if (lane < kStep) load4_lds(l.s, off_s, l.at + C::kBytesN + C::kBytesK + (uint32_t)wave * (kStep * 4));
+    }
+  };
+  auto load_stage = [&](int buffer) {
+    const Loads l = next_loads(buffer);
+#pragma unroll
+    for (int i = 0; i <= C::kLoads; ++i) load_piece(l, i);
   };
 
   // ---- fragments: lane l holds column l % 16 and rows 8 (l / 16) .. + 7
@@ -238,121 +264,157 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
       at_k[j] = (uint32_t)(C::kBytesN + row_n * C::kPitchK + ((wk * C::kFragK + j) ^ turn16(row_n)) * 32 + (lane & 3) * 8);
     }
   }
+  constexpr int kAhead = C::kPairs ? C::kStages - 4 : C::kStages - 2;   // stages on their way at a barrier
+  constexpr int kBegun = C::kPairs ? C::kStages - 1 : C::kStages;       // stages loaded before a tile's first
+  constexpr int kStores = kF32 ? C::kFragN * C::kFragK : C::kFragN * C::kFragK / 2;   // of a tile that lies whole in dW
   const uint32_t at_s = C::kBytesN + C::kBytesK + (uint32_t)(wk * C::kFragK / 8 * kStep + (lane >> 4) * 8) * 4;
 
-  auto frag16 = [&](DG_LAS uint8_t* a, int pitch) -> bf16x8 {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LAS s16x4*)a);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LAS s16x4*)(a + 4 * pitch));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-
   f32x4 acc[C::kFragN][C::kFragK];
-  bf16x8 fn[C::kFragN];
+  struct Pair16 {   // a fragment of 16-bit elements: rows 0 - 3 and 4 - 7 of a lane's 8
+    s16x4 lo, hi;
+  };
+  auto whole = [](const Pair16& f) -> bf16x8 {
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read16 = [&](DG_LAS uint8_t* a, int pitch, Pair16& f, int half) {
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DG_LAS s16x4*)(a + half * 4 * pitch));
+    if (half == 0) f.lo = v;
+    else f.hi = v;
+  };
+  Pair16 fn[C::kFragN];
   struct Right {   // x's fragments of a stage
-    bf16x8 f[C::kFragK];
+    u32x4 f[C::kFragK];
   };
   struct Raw {     // and what they are made of
-    i32x2 code[C::kFp8 ? C::kFragK : 1];
+    i32x2 code[C::kFragK];
+    Pair16 rows[C::kFragK];
     f32x4 scale[2];
   };
-  auto read_right = [&](DG_LAS uint8_t* stage, Raw& raw, Right& to) {
+  // x of a stage, one LDS read at a time, and a quarter of a fragment's conversion
+  constexpr int kReads = C::kFp8 ? 2 + C::kFragK : 2 * C::kFragK;
+  auto read_right = [&](DG_LAS uint8_t* stage, Raw& raw, int i) {
     if constexpr (C::kFp8) {
-#pragma unroll
-      for (int j = 0; j < C::kFragK; ++j)
-        raw.code[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((DG_LAS i32x2*)(stage + at_k[j]));
-      raw.scale[0] = *(DG_LAS f32x4*)(stage + at_s);
-      raw.scale[1] = *(DG_LAS f32x4*)(stage + at_s + 16);
+      if (i < 2) raw.scale[i] = *(DG_LAS f32x4*)(stage + at_s + 16 * i);
+      else raw.code[i - 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((DG_LAS i32x2*)(stage + at_k[i - 2]));
     } else {
-#pragma unroll
-      for (int j = 0; j < C::kFragK; ++j) to.f[j] = frag16(stage + at_k[j], C::kPitchK);
+      read16(stage + at_k[i >> 1], C::kPitchK, raw.rows[i >> 1], i & 1);
     }
   };
-  auto convert = [&](const Raw& raw, Right& to, int j) {
+  constexpr int kPieces = 4 * C::kFragK;
+  auto convert = [&](const Raw& raw, Right& to, int piece) {
+    const int j = piece >> 2, q = piece & 3;   // dword q of fragment j: rows 2 q and 2 q + 1
     if constexpr (C::kFp8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(raw.code[j][h], false);
-        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(raw.code[j][h], true);
-        w[2 * h] = pack_bf16x2(a[0] * raw.scale[h].x, a[1] * raw.scale[h].y);
-        w[2 * h + 1] = pack_bf16x2(b[0] * raw.scale[h].z, b[1] * raw.scale[h].w);
-      }
-      to.f[j] = __builtin_bit_cast(bf16x8, (u32x4){w[0], w[1], w[2], w[3]});
+      const f32x4 s = raw.scale[q >> 1];
+      const auto v = q & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(raw.code[j][q >> 1], true)
+                           : __builtin_amdgcn_cvt_pk_f32_fp8(raw.code[j][q >> 1], false);
+      to.f[j][q] = q & 1 ? pack_bf16x2(v[0] * s.z, v[1] * s.w) : pack_bf16x2(v[0] * s.x, v[1] * s.y);
+    } else if (q == 0) {
+      to.f[j] = __builtin_bit_cast(u32x4, whole(raw.rows[j]));
     }
   };
 
-  auto products = [&](int i, const Right& r) {
-#pragma unroll
-    for (int j = 0; j < C::kFragK; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r.f[j], fn[i], acc[i][j], 0, 0, 0);
-  };
   // One stage: products of the fragments in fn and `now`; those of the next stage (in `buffer`)
-  // come into fn and `next`.  `spent` is the buffer of this stage, which goes to the loads.
-  auto step = [&](const Right& now, Right& next, int spent, int buffer) {
+  // come into fn and `next`, and loads go to the buffer `spent`.  A step with a barrier waits until the stages read
+  // up to the next barrier have come in every wave, and until all waves have read the buffers that loads go
+  // to from then on.  A wave's instructions issue in order, so what the next stage needs stands between the
+  // products, a little after each.
+  constexpr int kSlots = C::kFragN * C::kFragK;
+  constexpr int kConvert = kSlots > 16 ? 12 : 11;   // first slot of a conversion: its codes are read by slot 9
+  auto step = [&](auto barrier, const Right& now, Right& next, int spent, int buffer, bool stored) {
     DG_LAS uint8_t* const stage = base + buffer * C::kStageBytes;
-    products(0, now);
-    __builtin_amdgcn_sched_barrier(0);
-    // the next stage's loads are done in every wave, and so are the reads of the spent one
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(C::kStages - 2) * C::kLoads>::value);
-    lds_barrier();
-    load_stage(spent);
+    const Loads loads = next_loads(spent);
     Raw raw;
-    read_right(stage, raw, next);
-    fn[0] = frag16(stage + at_n[0], C::kPitchN);
-    __builtin_amdgcn_sched_barrier(0);
+    static_for<0, kSlots>([&](auto slot) {
+      constexpr int q = slot, i = q / C::kFragK, j = q % C::kFragK;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.f[j]), whole(fn[i]), acc[i][j],
+                                                          0, 0, 0);
+      if constexpr (barrier && q == C::kFragK - 1) {
+        // stores of the tile before are younger than the loads of the first stages
+        if (stored) __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads + kStores>::value);
+        else __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads>::value);
+        lds_barrier();
+      }
+      static_for<0, C::kLoads + 1>([&](auto l) {
+        if constexpr (q == C::kFragK + 1 + l * ((kSlots - C::kFragK) / (C::kLoads + 1))) load_piece(loads, l);
+      });
+      if constexpr (q >= C::kFragK && q < C::kFragK + kReads) read_right(stage, raw, q - C::kFragK);
+      static_for<0, C::kFragN - 1>([&](auto f) {
+        constexpr int at = (f + 1) * C::kFragK + (f == 0 ? 4 : f == 1 ? 2 : 0);
+        if constexpr (q == at || q == at + 1) read16(stage + at_n[f], C::kPitchN, fn[f], q - at);
+      });
+      if constexpr (q >= kConvert)
+        static_for<(q - kConvert) * kPieces / (kSlots - kConvert), (q + 1 - kConvert) * kPieces / (kSlots - kConvert)>(
+            [&](auto piece) { convert(raw, next, piece); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    read16(stage + at_n[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 0);
+    read16(stage + at_n[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 1);
+  };
+
+  // Writes a tile; true if that took kStores stores and no loads.
+  auto put = [&](const Unit& w) -> bool {
+    const bool inside = w.n0 + C::kTn <= p.n && w.k0 + C::kTk <= p.k;
+    const int64_t n0 = w.n0 + wn * C::kFragN * 16 + (lane & 15), k0 = w.k0 + wk * C::kFragK * 16;
+    if (kF32 || p.splits > 1) {
+      // lane: row n = lane % 16 of fragment i, columns k = 4 (lane / 16) .. of fragment j
+      float* dw = p.splits > 1 ? p.partial + ((int64_t)w.split * p.groups + w.g) * p.n * p.k
+                               : (float*)p.dw + w.g * p.dw_gs;
+      const int64_t ld = p.splits > 1 ? p.k : p.lddw, k1 = k0 + (lane >> 4) * 4;
+      const bool add = p.accumulate && p.splits == 1;
+      auto each = [&](auto&& f) {
 #pragma unroll
-    for (int i = 1; i < C::kFragN; ++i) {
-      products(i, now);
-      fn[i] = frag16(stage + at_n[i], C::kPitchN);
-      // conversions follow the reads at some distance
+        for (int i = 0; i < C::kFragN; ++i) {
+          float* row = dw + (n0 + i * 16) * ld + k1;
 #pragma unroll
-      for (int j = 0; j < C::kFragK; ++j)
-        if (1 + j * (C::kFragN - 1) / C::kFragK == i)
-          convert(raw, next, j);
+          for (int j = 0; j < C::kFragK; ++j)
+            // k is a multiple of 8: four columns are in or out together
+            if (inside || (n0 + i * 16 < p.n && k1 + j * 16 < p.k)) f((f32x4*)(row + j * 16), acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);   // no more than a row's addresses and sums at once
+        }
+      };
+      // dW passes L2 by, which the operands need; the splits' sums are read again at once
+      if (add) each([&](f32x4* dst, f32x4 v) { *dst = *dst + v; });
+      else if (p.splits > 1) each([&](f32x4* dst, f32x4 v) { *dst = v; });
+      else each([&](f32x4* dst, f32x4 v) { __builtin_nontemporal_store(v, dst); });
+      return inside && !add && kF32;
+    }
+    // Two fragments side by side: lanes 16 apart exchange halves, so that each has eight columns in a row:
+    // 16 (lane / 16 % 2) + 8 (lane / 32) ..
+    uint16_t* dw = (uint16_t*)p.dw + w.g * p.dw_gs;
+    const int64_t k1 = k0 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+#pragma unroll
+    for (int i = 0; i < C::kFragN; ++i) {
+      uint16_t* row = dw + (n0 + i * 16) * p.lddw + k1;
+#pragma unroll
+      for (int j = 0; j < C::kFragK; j += 2) {
+        u32x4 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = pack_bf16x2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+          const uint32_t b = pack_bf16x2(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
+          const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+          v[h] = r[0];
+          v[2 + h] = r[1];
+        }
+        if (inside || (n0 + i * 16 < p.n && k1 + j * 16 < p.k))
+          __builtin_nontemporal_store(v, (u32x4*)(row + j * 16));
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-  };
-
-  auto put = [&](const Unit& w) {
-    // lane: row n = lane % 16 of fragment i, columns k = 4 (lane / 16) .. of fragment j
-    const int64_t n0 = w.n0 + wn * C::kFragN * 16 + (lane & 15), k0 = w.k0 + wk * C::kFragK * 16 + (lane >> 4) * 4;
-    const bool whole = w.n0 + C::kTn <= p.n && w.k0 + C::kTk <= p.k;
-    auto each = [&](auto&& f) {
-#pragma unroll
-      for (int i = 0; i < C::kFragN; ++i) {
-#pragma unroll
-        for (int j = 0; j < C::kFragK; ++j)
-          // k is a multiple of 8: four columns are in or out together
-          if (whole || (n0 + i * 16 < p.n && k0 + j * 16 < p.k)) f(acc[i][j], n0 + i * 16, k0 + j * 16);
-        __builtin_amdgcn_sched_barrier(0);   // no more than a row's addresses and sums at once
-      }
-    };
-    if (p.splits > 1) {
-      float* part = p.partial + ((int64_t)w.split * p.groups + w.g) * p.n * p.k;
-      each([&](f32x4 v, int64_t n, int64_t k) { *(f32x4*)(part + n * p.k + k) = v; });
-    } else if constexpr (kF32) {
-      float* dw = (float*)p.dw + w.g * p.dw_gs;
-      if (p.accumulate)
-        each([&](f32x4 v, int64_t n, int64_t k) {
-          f32x4* dst = (f32x4*)(dw + n * p.lddw + k);
-          *dst = *dst + v;
-        });
-      else
-        each([&](f32x4 v, int64_t n, int64_t k) { *(f32x4*)(dw + n * p.lddw + k) = v; });
-    } else {
-      uint16_t* dw = (uint16_t*)p.dw + w.g * p.dw_gs;
-      each([&](f32x4 v, int64_t n, int64_t k) {
-        *(u32x2*)(dw + n * p.lddw + k) = (u32x2){pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-      });
-    }
+    return inside;
   };
 
   const int grid = (int)gridDim.x;   // a multiple of 8
-  int u = (int)(blockIdx.x & 7) * (grid >> 3) + (int)(blockIdx.x >> 3);
+  const int mine = (int)(blockIdx.x & 7) * (grid >> 3) + (int)(blockIdx.x >> 3);
+  // unit of a round: forwards and backwards in turn, so that who gets the longest of one gets the shortest
+  // of the next (groups come in order of their rows)
+  auto unit_in = [&](int round) { return round * grid + (round & 1 ? grid - 1 - mine : mine); };
+  int round = 0, u = unit_in(0);
   if (u >= units) return;
   Unit w = unit_of(u);
   begin(w);
-  for (int s = 0; s < C::kStages; ++s) load_stage(s);
+  for (int s = 0; s < kBegun; ++s) load_stage(s);
+  bool stored = false;
   while (true) {
 #pragma unroll
     for (int i = 0; i < C::kFragN; ++i)
@@ -360,25 +422,32 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
       for (int j = 0; j < C::kFragK; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     if (w.stages > 0) {
       Right even, odd;
-      __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(C::kStages - 1) * C::kLoads>::value);
+      if (stored) __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(kBegun - 1) * C::kLoads + kStores>::value);
+      else __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(kBegun - 1) * C::kLoads>::value);
       lds_barrier();
       {
         Raw raw;
-        read_right(base, raw, even);
 #pragma unroll
-        for (int i = 0; i < C::kFragN; ++i) fn[i] = frag16(base + at_n[i], C::kPitchN);
+        for (int i = 0; i < kReads; ++i) read_right(base, raw, i);
 #pragma unroll
-        for (int j = 0; j < C::kFragK; ++j) convert(raw, even, j);
+        for (int i = 0; i < 2 * C::kFragN; ++i) read16(base + at_n[i >> 1], C::kPitchN, fn[i >> 1], i & 1);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) convert(raw, even, i);
       }
-      int buffer = 0;
+      int before = C::kStages - 1, buffer = 0;   // of the stage before and of this one
       auto after = [](int b) { return b + 1 == C::kStages ? 0 : b + 1; };
+      // stores are younger than the loads of stages 0 .. kBegun - 1; barriers of pairs wait for every other stage
+      int grace = stored ? (C::kPairs ? (kBegun - 1) / 2 : kBegun - 1) : 0;
       for (int s = 0;;) {
         int to = after(buffer);
-        step(even, odd, buffer, to);
+        step(std::true_type{}, even, odd, C::kPairs ? before : buffer, to, grace-- > 0);
+        before = buffer;
         buffer = to;
         if (++s == w.stages) break;
         to = after(buffer);
-        step(odd, even, buffer, to);
+        if constexpr (C::kPairs) step(std::false_type{}, odd, even, before, to, false);
+        else step(std::true_type{}, odd, even, buffer, to, grace-- > 0);
+        before = buffer;
         buffer = to;
         if (++s == w.stages) break;
       }
@@ -387,14 +456,14 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
     lds_barrier();
     const Unit last = w;
-    u += grid;
-    const bool more = u < units;
+    u = unit_in(++round);
+    const bool more = u < units;   // only the last round is not whole
     if (more) {
       w = unit_of(u);
       begin(w);
-      for (int s = 0; s < C::kStages; ++s) load_stage(s);
+      for (int s = 0; s < kBegun; ++s) load_stage(s);
     }
-    put(last);
+    stored = put(last);
     if (!more) break;
   }
 }
