@@ -39,12 +39,6 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax, int ue8m0) {
   return s;
 }
 
-// As fp8_scale from a maximum in which a NaN counts (magnitude): such a block's scale
-// is a NaN, which the products show.
-__device__ __forceinline__ float fp8_scale_or_nan(uint32_t amax, int ue8m0) {
-  return amax > 0x7F800000u ? __builtin_nanf("") : fp8_scale(amax, ue8m0);
-}
-
 __device__ __forceinline__ uint32_t fp8_of_four(const float* x, Divisor d) {
   float t[4];
 #pragma unroll
@@ -56,16 +50,40 @@ __device__ __forceinline__ uint32_t fp8_of_four(const float* x, Divisor d) {
 }
 
 // Codes of eight elements of a 128-wide block that 16 neighbouring lanes hold, and the
-// block's scale.
+// block's scale: the same bits as fp8_scale and fp8_of_four in fewer instructions, where every block takes
+// some thirty of them an element.  A NaN makes the scale a NaN (the maximum is the one that a NaN wins).  The
+// quotient of the division by 448 is corrected as in divide(); an infinite or NaN maximum is the scale itself.
+// No quotient exceeds 448 by more than its rounding (s is at least amax / 448 but for that), which the conversion
+// rounds back to 448, so nothing is clamped; codes under an infinite or NaN scale are unspecified.
 __device__ __forceinline__ u32x2 fp8_of_block(const float (&x)[8], int ue8m0, float& s) {
-  uint32_t amax = 0;
+  float m = __builtin_elementwise_maximum(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(x[i]));
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, 16));
-  s = fp8_scale_or_nan(amax, ue8m0);
+  for (int i = 2; i < 8; i += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(x[i])), fabsf(x[i + 1]));
+  uint32_t amax = magnitude(m);
+  // over the 16 lanes of a row of the wave, turned by 8, 4, 2 and 1: vector instructions, where shuffles go through LDS
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true));
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x124, 0xF, 0xF, true));
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x122, 0xF, 0xF, true));
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x121, 0xF, 0xF, true));
+  s = divide(fmaxf(__uint_as_float(amax), kAmaxFloor), {kE4M3Max, 1.0f / kE4M3Max});
+  if (ue8m0) {
+    uint32_t u = __float_as_uint(s);
+    if (u & 0x007FFFFFu) u = (u & 0x7F800000u) + 0x00800000u;
+    s = __uint_as_float(u);
+  }
+  if (amax >= 0x7F800000u) s = __uint_as_float(amax);
   const Divisor d{s, 1.0f / s};
-  return (u32x2){fp8_of_four(x, d), fp8_of_four(x + 4, d)};
+  u32x2 code;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __builtin_copysignf(divide(fabsf(x[4 * h + i]), d), x[4 * h + i]);
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+    code[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
+  }
+  return code;
 }
 
 // A row's int8 scale: a row with a NaN gets a NaN scale (and an infinite one an

@@ -60,22 +60,12 @@ __device__ __forceinline__ void weights_of(const void* w, int f32, int64_t c, fl
 
 constexpr int group_threads(int lanes) { return lanes > 256 ? lanes : 256; }
 
-// Groups of rows (a workgroup's) in runs per XCD: workgroup b runs on XCD b % 8, and
-// neighbouring rows' scales, 4 bytes each beside each other, meet in one L2.
-__device__ __forceinline__ int64_t run_of(int64_t b, int64_t n) {
-  const int64_t run = (n + 7) >> 3;
-  return (b & 7) * run + (b >> 3);
-}
-unsigned run_grid(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
-
 // kLanes lanes a row, eight columns each, kHeld times.
 template <class T, int kOut, int kLanes, int kHeld>
 __global__ void __launch_bounds__(group_threads(kLanes)) norm_kernel(NormParams p) {
   constexpr int kRows = group_threads(kLanes) / kLanes;
-  const int64_t groups = (p.rows + kRows - 1) / kRows;
-  const int64_t group = run_of(blockIdx.x, groups);
-  const int64_t r = group * kRows + threadIdx.x / kLanes;
-  if (group >= groups || r >= p.rows) return;   // with one row a workgroup all its waves leave
+  const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
+  if (r >= p.rows) return;   // with one row a workgroup all its waves leave
   const int lane = threadIdx.x % kLanes;
   __shared__ float part[kLanes / 64];
   __shared__ uint32_t top[kLanes / 64];
@@ -164,45 +154,63 @@ __global__ void __launch_bounds__(group_threads(kLanes)) norm_kernel(NormParams 
 }
 
 // A workgroup takes rows b, b + blocks, ... and keeps its share of dw in registers; rows
-// differ by kRows where a wave holds a row, and the waves' shares are added in order.
-template <class T, int kLanes, int kHeld>
-__global__ void __launch_bounds__(group_threads(kLanes)) norm_grad_kernel(NormGradParams p) {
+// differ by kRows where a wave holds a row, and the waves' shares are added in order.  kAhead: the loads of
+// the next row are issued before this row's sum, so that memory is busy through both.
+template <class T, int kLanes, int kHeld, bool kAhead>
+__global__ void __launch_bounds__(group_threads(kLanes), sizeof(typename T::store) == 2 && kAhead ? 4 : 1) norm_grad_kernel(NormGradParams p) {
   constexpr int kRows = group_threads(kLanes) / kLanes;
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   __shared__ float part[2][kLanes / 64];
   typedef typename T::store E;
+  struct Row {
+    Eight<T> g[kHeld], v[kHeld];
+    float rho;
+  };
+  auto load = [&](int64_t r, Row& row) {
+    const E* dy = (const E*)p.dy + r * p.lddy;
+    const E* h = (const E*)p.h + r * p.ldh;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int64_t c = (int64_t)(i * kLanes + lane) * 8;
+      const bool in = c < p.k;
+      row.g[i] = in ? stream_eight<T>(dy + c) : zero_eight<T>();
+      row.v[i] = in ? stream_eight<T>(h + c) : zero_eight<T>();
+    }
+    row.rho = p.rstd[r];
+  };
   float dw[kHeld][8];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * kRows + sub; r < p.rows; r += (int64_t)p.blocks * kRows) {
-    const E* dy = (const E*)p.dy + r * p.lddy;
-    const E* h = (const E*)p.h + r * p.ldh;
-    const E* dh = (const E*)p.dh + r * p.lddh;
-    Eight<T> g[kHeld], v[kHeld], u[kHeld];
+  const int64_t apart = (int64_t)p.blocks * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + sub;
+  Row now;
+  if (r < p.rows) load(r, now);
+  for (; r < p.rows; r += apart) {
+    Eight<T> u[kHeld];   // for the end of this row
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (int64_t)(i * kLanes + lane) * 8;
-      const bool in = c < p.k;
-      g[i] = in ? stream_eight<T>(dy + c) : zero_eight<T>();
-      v[i] = in ? stream_eight<T>(h + c) : zero_eight<T>();
-      u[i] = in && p.dh ? stream_eight<T>(dh + c) : zero_eight<T>();
+      u[i] = c < p.k && p.dh ? stream_eight<T>((const E*)p.dh + r * p.lddh + c) : zero_eight<T>();
     }
-    const float rho = p.rstd[r];
+    Row next;
+    if constexpr (kAhead) {
+      if (r + apart < p.rows) load(r + apart, next);
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (int64_t)(i * kLanes + lane) * 8;
       if (c >= p.k) continue;
       float a[8], b[8], w[8];
-      widen_eight(g[i], a);
-      widen_eight(v[i], b);
+      widen_eight(now.g[i], a);
+      widen_eight(now.v[i], b);
       weights_of<T>(p.weight, p.weight_f32, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = a[j] * (b[j] * rho);
+        const float t = a[j] * (b[j] * now.rho);
         dw[i][j] += t;
         dot = __builtin_fmaf(w[j], t, dot);
       }
@@ -216,13 +224,18 @@ __global__ void __launch_bounds__(group_threads(kLanes)) norm_grad_kernel(NormGr
       const int64_t c = (int64_t)(i * kLanes + lane) * 8;
       if (c >= p.k) continue;
       float a[8], b[8], w[8], e[8];
-      widen_eight(g[i], a);
-      widen_eight(v[i], b);
+      widen_eight(now.g[i], a);
+      widen_eight(now.v[i], b);
       widen_eight(u[i], e);
       weights_of<T>(p.weight, p.weight_f32, c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = __builtin_fmaf(rho, w[j] * a[j] - b[j] * rho * m, e[j]);
+      for (int j = 0; j < 8; ++j) e[j] = __builtin_fmaf(now.rho, w[j] * a[j] - b[j] * now.rho * m, e[j]);
       store_eight<T>(dx + c, e);
+    }
+    if constexpr (kAhead) {
+      now = next;
+    } else {
+      if (r + apart < p.rows) load(r + apart, now);
     }
   }
   if (!p.partial) return;
@@ -252,15 +265,22 @@ __global__ void __launch_bounds__(group_threads(kLanes)) norm_grad_kernel(NormGr
 }
 
 // dw[c] = sum of the workgroups' shares, in an order that their number alone gives: 16
-// columns a workgroup, 16 lanes a column.
-__global__ void __launch_bounds__(256) norm_weight_kernel(const float* partial, int64_t k, int blocks, float* dweight) {
+// columns a workgroup, 64 lanes a column.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial, int64_t k, int blocks, float* dweight) {
   const int64_t c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
   const int slice = threadIdx.x >> 4;
   float s = 0.0f;
   if (c < k)
-#pragma unroll 4
-    for (int b = slice; b < blocks; b += 16) s += partial[(int64_t)b * k + c];
-  __shared__ float part[16][17];
+#pragma unroll 8
+    for (int b = slice; b < blocks; b += 64) s += partial[(int64_t)b * k + c];
+  __shared__ float part[64][17];
+  part[slice][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (slice < 16) {
+#pragma unroll
+    for (int i = 16; i < 64; i += 16) s += part[slice + i][threadIdx.x & 15];
+  }
+  __syncthreads();
   part[slice][threadIdx.x & 15] = s;
   __syncthreads();
   if (slice == 0 && c < k) {
@@ -273,7 +293,7 @@ __global__ void __launch_bounds__(256) norm_weight_kernel(const float* partial, 
 template <class T, int kOut, int kLanes, int kHeld>
 void norm_of(const NormParams& p, hipStream_t stream) {
   constexpr int kRows = group_threads(kLanes) / kLanes;
-  hipLaunchKernelGGL((norm_kernel<T, kOut, kLanes, kHeld>), dim3(run_grid((p.rows + kRows - 1) / kRows)),
+  hipLaunchKernelGGL((norm_kernel<T, kOut, kLanes, kHeld>), dim3((unsigned)((p.rows + kRows - 1) / kRows)),
                      dim3(group_threads(kLanes)), 0, stream, p);
 }
 
@@ -298,9 +318,9 @@ hipError_t norm(const NormParams& p, int out, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-template <class T, int kLanes, int kHeld>
+template <class T, int kLanes, int kHeld, bool kAhead = true>
 void norm_grad_of(const NormGradParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_grad_kernel<T, kLanes, kHeld>), dim3((unsigned)p.blocks), dim3(group_threads(kLanes)), 0,
+  hipLaunchKernelGGL((norm_grad_kernel<T, kLanes, kHeld, kAhead>), dim3((unsigned)p.blocks), dim3(group_threads(kLanes)), 0,
                      stream, p);
 }
 
@@ -311,22 +331,24 @@ hipError_t norm_grad(const NormGradParams& p, hipStream_t stream) {
   else if (p.k <= 1024) norm_grad_of<T, 64, 2>(p, stream);
   else if (p.k <= 2048) norm_grad_of<T, 256, 1>(p, stream);
   else if (p.k <= 4096) norm_grad_of<T, 256, 2>(p, stream);
-  else if (p.k <= 8192) norm_grad_of<T, 1024, 1>(p, stream);
-  else norm_grad_of<T, 1024, 2>(p, stream);
+  else if (p.k <= 8192) norm_grad_of<T, 512, 2>(p, stream);
+  else norm_grad_of<T, 1024, 2, false>(p, stream);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.dweight) return err;
-  hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)((p.k + 15) / 16)), dim3(256), 0, stream, p.partial, p.k,
+  hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)((p.k + 15) / 16)), dim3(1024), 0, stream, p.partial, p.k,
                      p.blocks, p.dweight);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// As many as run at once, each with the same number of rows but for the last few.
 int norm_grad_blocks(int64_t rows, int64_t k) {
   const int64_t at_once = k <= 1024 ? 4 : 1;   // rows that a workgroup takes together
   const int64_t need = (rows + at_once - 1) / at_once;
-  const int64_t most = 1024;
-  return (int)(need < 1 ? 1 : need < most ? need : most);
+  const int64_t most = k <= 2048 ? 1536 : k <= 4096 ? 1024 : 512;
+  const int64_t turns = (need + most - 1) / most;
+  return (int)(need < 1 ? 1 : (need + turns - 1) / turns);
 }
 
 hipError_t launch_norm(const NormParams& p, int dtype, int out, hipStream_t stream) {

@@ -63,31 +63,68 @@ __device__ __forceinline__ void each_piece(const RowSet& at, int64_t per_row, F&
   }
 }
 
-__device__ __forceinline__ void put_codes(uint8_t* q, float* sf, int64_t s0, int64_t s1, int64_t r, int64_t c, u32x2 code,
-                                          float s) {
-  __builtin_nontemporal_store(code, (u32x2*)(q + c));
-  if ((threadIdx.x & 15) == 0) sf[r * s0 + (c >> 7) * s1] = s;
+// The same where blocks of 128 columns are cast: a workgroup takes 16 rows of kAtOnce neighbouring blocks, so that what
+// it writes are whole lines of codes and, where a block's scales lie beside each other along the rows, 64 bytes of
+// them.  f(row, first column, columns that are left): kAtOnce pieces 128 apart, all of whose loads
+// are issued before the first is used.
+template <int kAtOnce, class F>
+__device__ __forceinline__ void each_block(const RowSet& at, int64_t inner, F&& f) {
+  const int64_t g = blockIdx.y, rows = rows_in(at, g);
+  const int64_t across = (inner + 128 * kAtOnce - 1) / (128 * kAtOnce);
+  const int64_t units = (rows + 15) / 16 * across;
+  for (int64_t b = blockIdx.x; b < units; b += gridDim.x) {
+    const int64_t set = b / across, in = set * 16 + (threadIdx.x >> 4), r = g * at.group_rows + in;
+    const int64_t c = (b - set * across) * (128 * kAtOnce) + (threadIdx.x & 15) * 8;
+    if (in < rows && (!at.m_indices || at.m_indices[r] >= 0)) f(r, c, inner - c);
+  }
 }
 
-// inner is a multiple of 128, so a row is a multiple of 16 pieces and the 16 lanes of a
-// block are in the same row.
-template <class T, bool kKeep>
+__device__ __forceinline__ void put_codes(uint8_t* q, u32x2 code) { __builtin_nontemporal_store(code, (u32x2*)q); }
+
+// Scales of the blocks that a row's 16 lanes cast together, side by side: one lane each writes them, in one
+// store.
+struct ScaleOut {
+  float* at;       // this lane's
+  int64_t step;    // to the next block's
+  __device__ __forceinline__ void put(int blocks, float s0, float s1, float s2) const {
+    const int l = threadIdx.x & 15;
+    if (l < blocks) *at = l == 0 ? s0 : l == 1 ? s1 : s2;
+  }
+};
+
+template <class T, bool kKeep, int kAtOnce>
 __global__ void __launch_bounds__(kThreads) swiglu_fp8_kernel(SwigluParams p) {
   typedef typename T::store E;
-  each_piece(p.at, p.inner / 8, [&](int64_t r, int64_t c) {
+  each_block<kAtOnce>(p.at, p.inner, [&](int64_t r, int64_t c, int64_t left) {
     const E* h = (const E*)p.h + r * p.ldh + c;
-    float g[8], u[8], a[8], s;
-    widen_eight(stream_eight<T>(h), g);
-    widen_eight(stream_eight<T>(h + p.inner), u);
+    Eight<T> hg[kAtOnce], hu[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = silu(g[i]) * u[i];
-    const u32x2 code = fp8_of_block(a, p.ue8m0, s);
-    put_codes(p.q + r * p.ldq, p.sf, p.sf_s0, p.sf_s1, r, c, code, s);
-    if constexpr (kKeep) {
-      const u32x2 cg = fp8_of_block(g, p.ue8m0, s);
-      put_codes(p.hq + r * p.ldhq, p.hsf, p.hsf_s0, p.hsf_s1, r, c, cg, s);
-      const u32x2 cu = fp8_of_block(u, p.ue8m0, s);
-      put_codes(p.hq + r * p.ldhq, p.hsf, p.hsf_s0, p.hsf_s1, r, c + p.inner, cu, s);
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i * 128 < left) {   // the same for the whole workgroup
+        hg[i] = stream_eight<T>(h + i * 128);
+        hu[i] = stream_eight<T>(h + p.inner + i * 128);
+      }
+    }
+    const int l = threadIdx.x & 15;
+    uint8_t* q = p.q + r * p.ldq + c;
+    uint8_t* hq = kKeep ? p.hq + r * p.ldhq + c : nullptr;
+    ScaleOut out{p.sf + r * p.sf_s0 + (c >> 7) * p.sf_s1, p.sf_s1};
+    if (kKeep && l > 0) out = {p.hsf + r * p.hsf_s0 + ((c + (l > 1 ? p.inner : 0)) >> 7) * p.hsf_s1, p.hsf_s1};
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i * 128 >= left) break;
+      float g[8], u[8], a[8], sa, sg = 0.0f, su = 0.0f;
+      widen_eight(hg[i], g);
+      widen_eight(hu[i], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = silu(g[j]) * u[j];
+      put_codes(q + i * 128, fp8_of_block(a, p.ue8m0, sa));
+      if constexpr (kKeep) {
+        put_codes(hq + i * 128, fp8_of_block(g, p.ue8m0, sg));
+        put_codes(hq + p.inner + i * 128, fp8_of_block(u, p.ue8m0, su));
+      }
+      out.put(kKeep ? 3 : 1, sa, sg, su);
+      out.at += out.step;
     }
   });
 }
@@ -140,25 +177,44 @@ __global__ void __launch_bounds__(kThreads) swiglu_int8_kernel(SwigluParams p) {
   }
 }
 
-template <class T, bool kCodes, bool kCast>
+// Eight columns of both halves and of the gradient, as they are stored.
+template <class T, bool kCodes>
+struct GradIn {
+  Eight<T> d;
+  Eight<T> g, u;     // from h,
+  u32x2 qg, qu;      // or from the checkpoint
+  float sg, su;
+};
+
+template <class T, bool kCodes, bool kCast, int kAtOnce>
 __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(SwigluGradParams p) {
   typedef typename T::store E;
-  each_piece(p.at, p.inner / 8, [&](int64_t r, int64_t c) {
-    float d[8], g[8], u[8];
+  typedef GradIn<T, kCodes> In;
+  auto load = [&](int64_t r, int64_t c, In& in) {
+    in.d = stream_eight<T>((const E*)p.da + r * p.ldda + c);
     if constexpr (kCodes) {
       const uint8_t* q = p.hq + r * p.ldhq + c;
       const float* sf = p.hsf + r * p.hsf_s0;
-      const u32x2 qg = __builtin_nontemporal_load((const u32x2*)q);
-      const u32x2 qu = __builtin_nontemporal_load((const u32x2*)(q + p.inner));
-      const float sg = sf[(c >> 7) * p.hsf_s1], su = sf[((c + p.inner) >> 7) * p.hsf_s1];
-      widen_codes(qg, sg, g);
-      widen_codes(qu, su, u);
+      in.qg = __builtin_nontemporal_load((const u32x2*)q);
+      in.qu = __builtin_nontemporal_load((const u32x2*)(q + p.inner));
+      in.sg = sf[(c >> 7) * p.hsf_s1];
+      in.su = sf[((c + p.inner) >> 7) * p.hsf_s1];
     } else {
       const E* h = (const E*)p.h + r * p.ldh + c;
-      widen_eight(stream_eight<T>(h), g);
-      widen_eight(stream_eight<T>(h + p.inner), u);
+      in.g = stream_eight<T>(h);
+      in.u = stream_eight<T>(h + p.inner);
     }
-    widen_eight(stream_eight<T>((const E*)p.da + r * p.ldda + c), d);
+  };
+  auto finish = [&](E* dh, uint8_t* q, const ScaleOut& out, const In& in) {
+    float d[8], g[8], u[8];
+    widen_eight(in.d, d);
+    if constexpr (kCodes) {
+      widen_codes(in.qg, in.sg, g);
+      widen_codes(in.qu, in.su, u);
+    } else {
+      widen_eight(in.g, g);
+      widen_eight(in.u, u);
+    }
     float dg[8], du[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -167,17 +223,40 @@ __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(SwigluGradParams 
       du[i] = d[i] * gs;
       dg[i] = d[i] * u[i] * __builtin_fmaf(gs, 1.0f - s, s);
     }
-    E* dh = (E*)p.dh + r * p.lddh + c;
     store_eight<T>(dh, dg);
     store_eight<T>(dh + p.inner, du);
     if constexpr (kCast) {
-      float s;
-      const u32x2 cg = fp8_of_block(dg, p.ue8m0, s);
-      put_codes(p.q + r * p.ldq, p.sf, p.sf_s0, p.sf_s1, r, c, cg, s);
-      const u32x2 cu = fp8_of_block(du, p.ue8m0, s);
-      put_codes(p.q + r * p.ldq, p.sf, p.sf_s0, p.sf_s1, r, c + p.inner, cu, s);
+      float sg, su;
+      put_codes(q, fp8_of_block(dg, p.ue8m0, sg));
+      put_codes(q + p.inner, fp8_of_block(du, p.ue8m0, su));
+      out.put(2, sg, su, 0.0f);
     }
-  });
+  };
+  if constexpr (kCodes || kCast) {
+    each_block<kAtOnce>(p.at, p.inner, [&](int64_t r, int64_t c, int64_t left) {
+      In in[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (i * 128 < left) load(r, c + i * 128, in[i]);
+      E* dh = (E*)p.dh + r * p.lddh + c;
+      uint8_t* q = kCast ? p.q + r * p.ldq + c : nullptr;
+      ScaleOut out{};
+      if constexpr (kCast)
+        out = {p.sf + r * p.sf_s0 + ((c + (threadIdx.x & 15 ? p.inner : 0)) >> 7) * p.sf_s1, p.sf_s1};
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i * 128 >= left) break;
+        finish(dh + i * 128, q + i * 128, out, in[i]);
+        out.at += out.step;
+      }
+    });
+  } else {
+    each_piece(p.at, p.inner / 8, [&](int64_t r, int64_t c) {
+      In in;
+      load(r, c, in);
+      finish((E*)p.dh + r * p.lddh + c, nullptr, {}, in);
+    });
+  }
 }
 
 // Workgroups a group gets: all its pieces at once, less where there are many groups, whose
@@ -189,11 +268,25 @@ dim3 grid_of(const RowSet& at, int64_t items, int64_t per_block) {
   return dim3((unsigned)x, (unsigned)at.groups);
 }
 
+// Blocks of 128 columns that a workgroup takes at once.
+constexpr int kMany = 4;
+bool many_blocks(const RowSet& at, int64_t inner) { return at.group_rows * at.groups * inner >= (int64_t)1 << 24; }
+dim3 block_grid(const RowSet& at, int64_t inner, int at_once) {
+  return grid_of(at, (at.group_rows + 15) / 16 * ((inner + 128 * at_once - 1) / (128 * at_once)), 1);
+}
+
+template <class T, bool kKeep>
+void swiglu_fp8_of(const SwigluParams& p, hipStream_t stream) {
+  if (many_blocks(p.at, p.inner))
+    hipLaunchKernelGGL((swiglu_fp8_kernel<T, kKeep, kMany>), block_grid(p.at, p.inner, kMany), dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((swiglu_fp8_kernel<T, kKeep, 1>), block_grid(p.at, p.inner, 1), dim3(kThreads), 0, stream, p);
+}
+
 template <class T>
 hipError_t swiglu_fp8(const SwigluParams& p, hipStream_t stream) {
-  const dim3 grid = grid_of(p.at, p.at.group_rows * (p.inner / 8), kThreads);
-  if (p.hq) hipLaunchKernelGGL((swiglu_fp8_kernel<T, true>), grid, dim3(kThreads), 0, stream, p);
-  else hipLaunchKernelGGL((swiglu_fp8_kernel<T, false>), grid, dim3(kThreads), 0, stream, p);
+  if (p.hq) swiglu_fp8_of<T, true>(p, stream);
+  else swiglu_fp8_of<T, false>(p, stream);
   return hipGetLastError();
 }
 
@@ -208,16 +301,26 @@ hipError_t swiglu_int8(const SwigluParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <class T, bool kCodes, bool kCast>
+void swiglu_grad_of(const SwigluGradParams& p, hipStream_t stream) {
+  if constexpr (!kCodes && !kCast) {
+    hipLaunchKernelGGL((swiglu_grad_kernel<T, false, false, 1>), grid_of(p.at, p.at.group_rows * (p.inner / 8), kThreads),
+                       dim3(kThreads), 0, stream, p);
+  } else if (many_blocks(p.at, p.inner)) {
+    hipLaunchKernelGGL((swiglu_grad_kernel<T, kCodes, kCast, kMany>), block_grid(p.at, p.inner, kMany), dim3(kThreads), 0,
+                       stream, p);
+  } else {
+    hipLaunchKernelGGL((swiglu_grad_kernel<T, kCodes, kCast, 1>), block_grid(p.at, p.inner, 1), dim3(kThreads), 0, stream,
+                       p);
+  }
+}
+
 template <class T>
 hipError_t swiglu_grad(const SwigluGradParams& p, hipStream_t stream) {
-  const dim3 grid = grid_of(p.at, p.at.group_rows * (p.inner / 8), kThreads), block(kThreads);
-  if (p.hq) {
-    if (p.q) hipLaunchKernelGGL((swiglu_grad_kernel<T, true, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((swiglu_grad_kernel<T, true, false>), grid, block, 0, stream, p);
-  } else {
-    if (p.q) hipLaunchKernelGGL((swiglu_grad_kernel<T, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((swiglu_grad_kernel<T, false, false>), grid, block, 0, stream, p);
-  }
+  if (p.hq && p.q) swiglu_grad_of<T, true, true>(p, stream);
+  else if (p.hq) swiglu_grad_of<T, true, false>(p, stream);
+  else if (p.q) swiglu_grad_of<T, false, true>(p, stream);
+  else swiglu_grad_of<T, false, false>(p, stream);
   return hipGetLastError();
 }
 
