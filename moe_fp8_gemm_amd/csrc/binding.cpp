@@ -461,7 +461,8 @@ struct Codes {
 };
 Codes fp8_out(const Args& a, int q, int sf, int64_t rows, int64_t k, const Tensor& like) {
   return {output(a, q, "q", {rows, k}, at::kFloat8_e4m3fn, kE4M3 | kU8, like),
-          a.none(sf) ? fresh({k / 128, rows}, at::kFloat, like).t() : scales(a, sf, "sf", {rows, k / 128})};
+          a.none(sf) ? at::detail::empty_strided_cuda({rows, k / 128}, {1, rows}, at::kFloat, like.device())
+                     : scales(a, sf, "sf", {rows, k / 128})};
 }
 
 // kind 0: rows, 1: FP8, 2: int8.  (x, weight, residual, eps, [ue8m0, q, sf | q, sf], y, h, rstd)

@@ -29,6 +29,15 @@ __device__ __forceinline__ float divide(float x, Divisor d) {
   return __builtin_fmaf(rem, d.y, q);
 }
 
+// The same with the remainder's sign turned, which keeps the sign of a zero: q s - x of a zero x is +0, and
+// q - 0 y has q's sign.
+__device__ __forceinline__ float divide_signed(float x, Divisor d) {
+#pragma clang fp contract(off)
+  const float q = x * d.y;
+  const float rem = __builtin_fmaf(q, d.s, -x);
+  return __builtin_fmaf(-rem, d.y, q);
+}
+
 __device__ __forceinline__ float fp8_scale(uint32_t amax, int ue8m0) {
   float s = fmaxf(__uint_as_float(amax), kAmaxFloor) / kE4M3Max;
   if (ue8m0) {
@@ -79,7 +88,7 @@ __device__ __forceinline__ u32x2 fp8_of_block(const float (&x)[8], int ue8m0, fl
   for (int h = 0; h < 2; ++h) {
     float t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = __builtin_copysignf(divide(fabsf(x[4 * h + i]), d), x[4 * h + i]);
+    for (int i = 0; i < 4; ++i) t[i] = divide_signed(x[4 * h + i], d);
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
     code[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], v, true);
   }

@@ -303,7 +303,8 @@ hipError_t norm(const NormParams& p, hipStream_t stream) {
   else if (p.k <= 1024) norm_of<T, kOut, 64, 2>(p, stream);
   else if (p.k <= 2048) norm_of<T, kOut, 256, 1>(p, stream);
   else if (p.k <= 4096) norm_of<T, kOut, 256, 2>(p, stream);
-  else if (p.k <= 8192) norm_of<T, kOut, 256, 4>(p, stream);
+  else if (p.k <= 8192 && p.rows > 256) norm_of<T, kOut, 256, 4>(p, stream);
+  else if (p.k <= 8192) norm_of<T, kOut, 1024, 1>(p, stream);   // a row a CU: as many lanes as there are
   else norm_of<T, kOut, 1024, 2>(p, stream);
   return hipGetLastError();
 }
@@ -346,7 +347,7 @@ hipError_t norm_grad(const NormGradParams& p, hipStream_t stream) {
 int norm_grad_blocks(int64_t rows, int64_t k) {
   const int64_t at_once = k <= 1024 ? 4 : 1;   // rows that a workgroup takes together
   const int64_t need = (rows + at_once - 1) / at_once;
-  const int64_t most = k <= 2048 ? 1536 : k <= 4096 ? 1024 : 512;
+  const int64_t most = k <= 2048 ? 1024 : k <= 4096 ? 1024 : 512;
   const int64_t turns = (need + most - 1) / most;
   return (int)(need < 1 ? 1 : (need + turns - 1) / turns);
 }

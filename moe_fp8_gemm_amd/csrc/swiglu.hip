@@ -6,8 +6,8 @@
 // FP8 cast of h itself, in blocks of 128 that do not straddle the halves.  Gradient, at the stored h
 // or at the values that the checkpoint stands for:
 //   dg = da u s (1 + g (1 - s)),   du = da g s.
-// e^-g is the hardware's 2^x of a rounded product: its relative error is |g| 2^-24 and a few
-// units of the last place, far below a code or a 16-bit result.
+// e^-g is the hardware's 2^x of the rounded product t = -g log2 e, times 1 + (-g - t ln 2) for what the rounding
+// left out, so that its relative error is a few units of the last place at any g.
 //
 // Bound by memory: each element is read once and written once, in 16-byte pieces (8 bytes of
 // codes).  A layout's rows without a token are skipped: m_indices marks them row by row,
@@ -21,8 +21,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Beyond 88 the sigmoid is 1, or below fp32's normal numbers; a NaN comes back with the gate itself, which is a
+// factor of everything below.
 __device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+  const float c = __builtin_amdgcn_fmed3f(g, -88.0f, 88.0f);
+  const float t = c * -1.44269504088896341f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float d = 1.0f + __builtin_fmaf(e, __builtin_fmaf(t, -0.693147180559945309f, -c), e);
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);   // within half a unit of the last place or little more
 }
 // g s: a gate of -1e30 gives 0, not -1e30 * 0 of an underflow in the wrong place
 __device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
@@ -269,7 +276,7 @@ dim3 grid_of(const RowSet& at, int64_t items, int64_t per_block) {
 }
 
 // Blocks of 128 columns that a workgroup takes at once.
-constexpr int kMany = 4;
+constexpr int kMany = 2;
 bool many_blocks(const RowSet& at, int64_t inner) { return at.group_rows * at.groups * inner >= (int64_t)1 << 24; }
 dim3 block_grid(const RowSet& at, int64_t inner, int at_once) {
   return grid_of(at, (at.group_rows + 15) / 16 * ((inner + 128 * at_once - 1) / (128 * at_once)), 1);

@@ -112,6 +112,19 @@ def test_norm(m, k, dtype):
     assert torch.equal(gh2.cpu(), x)
 
 
+def test_signs_of_zeros_and_of_what_rounds_to_them():
+    """The casts keep them, as the plain ones do: codes 0x00 and 0x80."""
+    x = torch.zeros((2, 256))
+    x[0, ::2], x[1, 1::3], x[1, 5], x[1, 200] = -0.0, -1e-30, 2.0, -3.0
+    h = torch.cat([x, torch.ones(2, 256)], 1)
+    _, (hq, hs) = dg.swiglu_checkpoint_fp8(h.to(device()))
+    oq, osf = quant.per_token_cast(h.numpy())
+    assert np.array_equal(codes(hq), oq) and np.array_equal(hs.cpu().numpy(), osf) and (oq == 0x80).sum() > 200
+    y = torch.empty((2, 256), device=device())
+    (q, sf), _, _ = dg.rms_norm_cast_fp8(x.to(device()), y=y, eps=1e-3)
+    assert np.array_equal(codes(q), quant.per_token_cast(y.cpu().numpy())[0]) and (codes(q) == 0x80).sum() > 200
+
+
 def test_norm_in_place_and_outputs_that_are_given():
     x, r, w, h = norm_inputs(37, 2048, BF16, 5)
     want = dg.rms_norm(x.to(device()), w.to(device()), r.to(device()))
