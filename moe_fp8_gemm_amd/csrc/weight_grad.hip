@@ -15,7 +15,19 @@
 //
 // Pipeline.  All other stages of LDS are in flight; a step multiplies the fragments of one stage, held in
 // registers, while it reads those of the next into the registers that it has just used (codes are converted on the
-// way), and a barrier every step or every other hands the buffers of the stages before to the loads.
+// way), and a barrier every step or every other hands the buffers of the stages before to the loads.  Stages follow
+// one another across big tiles: while the last stages of one are multiplied and its sums are stored, the
+// next one's are on their way.
+//
+// Bound by matrix instructions, at the clock that the card's power leaves them (1.9 to 2.2 GHz), where groups have
+// many rows, and by the operands' and dW's way through memory where they have few.  Measured, with operands that no
+// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 577 us with fp32 sums (835 TFLOP/s, 940 MB of dW) and
+// 488 us in bf16 (985), 16-bit rows 570 and 466 us; 64 experts, 16384 rows, 2048 x 1408: codes 257 and 172 us
+// (738 MB of fp32, 369 of bf16), 16-bit rows 281 and 189 us; a dense 8191 x 512 x 2176 in 34 us.
+// Each tile with a prologue of its own: 600 and 507, 260 and 199 us (codes).
+//
+// Tried: the 32 x 32 x 16 instruction takes 11% fewer cycles a stage, and the clock falls by 14%; two workgroups of
+// 256 x 128 a CU 977 TFLOP/s where one of 256 x 256 does 1062 (4096^3, 16-bit rows 1014 and 1173).
 #include "dgfp8_device.h"
 #include "layer_internal.h"
 
@@ -35,8 +47,13 @@ struct Config {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kWaves = kWavesN * kWavesK, kThreads = kWaves * 64;
   static constexpr int kFragN = kTn / kWavesN / 16, kFragK = kTk / kWavesK / 16;
-  // with four stages or fewer a barrier every step keeps more loads on their way than one every other step
+  // A barrier every other step spares a wave the other half (codes, six stages: 1766 cycles a stage and 1876), but with
+  // four stages or fewer it leaves too few loads on their way (16-bit rows: 1597 and 1460).
   static constexpr bool kPairs = kStages > 4;
+  // The loads go on to the next tile while this one is finished (64 experts of 256 rows, 2048 x 1408: 199 -> 172 us).
+  // Small tiles are all at work at once: a workgroup has one, and the look for the next would cost it 4 to 8%
+  // (8191 rows, 512 x 2176: 33 -> 34.5 us).
+  static constexpr bool kAcross = kTn >= 256;
   static constexpr int kPitchN = kTn * 2, kPitchK = kTk * (kFp8 ? 1 : 2);   // bytes of an LDS row
   static constexpr int kBytesN = kStep * kPitchN, kBytesK = kStep * kPitchK;
   static constexpr int kBlocks = kTk / 128;
@@ -132,7 +149,7 @@ struct Unit {
 template <class C, bool kF32>
 __global__ void __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[C::kStages * C::kStageBytes];
+  __shared__ __attribute__((aligned(256))) uint8_t lds[C::kStages * C::kStageBytes];
   __shared__ int32_t group_first[kMaxGroups], group_count[kMaxGroups];
   __shared__ int16_t group_order[kMaxGroups];
   DG_LAS uint8_t* const base = (DG_LAS uint8_t*)lds;
@@ -197,7 +214,15 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
   }
   const uint32_t off_s = C::kFp8 ? (uint32_t)lane * (uint32_t)(p.sf_s0 * 4) : 0;   // lanes 0 .. 31: a block's rows
 
-  // where the next stage comes from
+  const int grid = (int)gridDim.x;   // a multiple of 8
+  const int mine = (int)(blockIdx.x & 7) * (grid >> 3) + (int)(blockIdx.x >> 3);
+  // unit of a round: forwards and backwards in turn, so that who gets the longest of one gets the shortest
+  // of the next (groups come in order of their rows)
+  auto unit_in = [&](int round) { return round * grid + (round & 1 ? grid - 1 - mine : mine); };
+  if (unit_in(0) >= units) return;
+
+  // where the next stage comes from: the loads walk through the units on their own, ahead of the products
+  int load_round = 0, load_left = 0;   // the next unit's round; stages that the present one still has
   uint64_t src_n = 0, src_k = 0, src_s = 0;
   int src_left = 0;
   uint32_t cols_n = 0, cols_k = 0;
@@ -220,6 +245,18 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     uint32_t at;
   };
   auto next_loads = [&](int buffer) -> Loads {
+    // on to the next unit that has rows; behind the last one nothing is left, and the loads write zeros
+    if constexpr (C::kAcross) {
+      while (__builtin_expect(load_left == 0, 0)) {
+        const int u = unit_in(load_round);
+        if (u >= units) break;
+        ++load_round;
+        const Unit w = unit_of(u);
+        load_left = w.stages;
+        if (load_left > 0) begin(w);
+      }
+      if (load_left > 0) --load_left;
+    }
     const uint32_t rows = src_left > kStep ? kStep : src_left < 0 ? 0 : src_left;
     const uint32_t s0 = C::kFp8 ? (uint32_t)(p.sf_s0 * 4) : 0;
     Loads l;
@@ -251,19 +288,17 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
 
   // ---- fragments: lane l holds column l % 16 and rows 8 (l / 16) .. + 7
   const int row_n = (lane >> 4) * 8 + ((lane & 15) >> 2);   // and row_n + 4
-  uint32_t at_n[C::kFragN], at_k[C::kFragK];
-#pragma unroll
-  for (int i = 0; i < C::kFragN; ++i)
-    at_n[i] = (uint32_t)row_n * C::kPitchN + (uint32_t)(((wn * C::kFragN + i) ^ turn16(row_n)) * 32 + (lane & 3) * 8);
-#pragma unroll
-  for (int j = 0; j < C::kFragK; ++j) {
-    if constexpr (C::kFp8) {
-      const int r = (lane >> 4) * 8 + ((lane & 15) >> 1);
-      at_k[j] = (uint32_t)(C::kBytesN + r * C::kPitchK + ((wk * C::kFragK + j) ^ turn8<C::kPitchK>(r)) * 16 + (lane & 1) * 8);
-    } else {
-      at_k[j] = (uint32_t)(C::kBytesN + row_n * C::kPitchK + ((wk * C::kFragK + j) ^ turn16(row_n)) * 32 + (lane & 3) * 8);
-    }
-  }
+  // Where a wave's first fragments lie in a stage.  The others' units differ from theirs in the bits of their number,
+  // which stand in bits of the address that no sum carries into: xor gives them.
+  auto place16 = [&](int unit, int pitch) {
+    return (uint32_t)(row_n * pitch + ((unit ^ turn16(row_n)) << 5) + (lane & 3) * 8);
+  };
+  const uint32_t at_n = place16(wn * C::kFragN, C::kPitchN);
+  const int row_c = (lane >> 4) * 8 + ((lane & 15) >> 1);   // of codes
+  const uint32_t at_k = C::kBytesN + (C::kFp8 ? (uint32_t)(row_c * C::kPitchK + ((wk * C::kFragK ^ turn8<C::kPitchK>(row_c)) << 4) +
+                                                          (lane & 1) * 8)
+                                              : place16(wk * C::kFragK, C::kPitchK));
+  static_assert(C::kStageBytes % (C::kFragN * 32) == 0 && C::kBytesN % 256 == 0, "units' bits stay clear of sums");
   constexpr int kAhead = C::kPairs ? C::kStages - 4 : C::kStages - 2;   // stages on their way at a barrier
   constexpr int kBegun = C::kPairs ? C::kStages - 1 : C::kStages;       // stages loaded before a tile's first
   constexpr int kStores = kF32 ? C::kFragN * C::kFragK : C::kFragN * C::kFragK / 2;   // of a tile that lies whole in dW
@@ -282,6 +317,11 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     else f.hi = v;
   };
   Pair16 fn[C::kFragN];
+  uint32_t an[C::kFragN], ak[C::kFragK];
+#pragma unroll
+  for (int i = 0; i < C::kFragN; ++i) an[i] = at_n ^ (i << 5);
+#pragma unroll
+  for (int i = 0; i < C::kFragK; ++i) ak[i] = at_k ^ (i << (C::kFp8 ? 4 : 5));
   struct Right {   // x's fragments of a stage
     u32x4 f[C::kFragK];
   };
@@ -295,9 +335,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
   auto read_right = [&](DG_LAS uint8_t* stage, Raw& raw, int i) {
     if constexpr (C::kFp8) {
       if (i < 2) raw.scale[i] = *(DG_LAS f32x4*)(stage + at_s + 16 * i);
-      else raw.code[i - 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((DG_LAS i32x2*)(stage + at_k[i - 2]));
+      else raw.code[i - 2] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((DG_LAS i32x2*)(stage + ak[i - 2]));
     } else {
-      read16(stage + at_k[i >> 1], C::kPitchK, raw.rows[i >> 1], i & 1);
+      read16(stage + ak[i >> 1], C::kPitchK, raw.rows[i >> 1], i & 1);
     }
   };
   constexpr int kPieces = 4 * C::kFragK;
@@ -313,26 +353,29 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     }
   };
 
-  // One stage: products of the fragments in fn and `now`; those of the next stage (in `buffer`)
-  // come into fn and `next`, and loads go to the buffer `spent`.  A step with a barrier waits until the stages read
-  // up to the next barrier have come in every wave, and until all waves have read the buffers that loads go
-  // to from then on.  A wave's instructions issue in order, so what the next stage needs stands between the
-  // products, a little after each.
+  // One stage: products of the fragments in fn and `now`; those of the next stage (in `buffer`) come into fn and
+  // `next`, and loads go to the buffer `spent`; where a big tile ends, both are the next tile's.  A step with a
+  // barrier waits until the stages read up to the next barrier have come in every wave, and until all waves have read
+  // the buffers that loads go to from then on.  A wave's instructions issue in order, so what the next stage needs
+  // stands between the products, a little after each.
   constexpr int kSlots = C::kFragN * C::kFragK;
   constexpr int kConvert = kSlots > 16 ? 12 : 11;   // first slot of a conversion: its codes are read by slot 9
-  auto step = [&](auto barrier, const Right& now, Right& next, int spent, int buffer, bool stored) {
+  auto step = [&](bool barrier, const Right& now, Right& next, int spent, int buffer, bool stored) {
     DG_LAS uint8_t* const stage = base + buffer * C::kStageBytes;
-    const Loads loads = next_loads(spent);
+    Loads loads;
     Raw raw;
     static_for<0, kSlots>([&](auto slot) {
       constexpr int q = slot, i = q / C::kFragK, j = q % C::kFragK;
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.f[j]), whole(fn[i]), acc[i][j],
                                                           0, 0, 0);
-      if constexpr (barrier && q == C::kFragK - 1) {
-        // stores of the tile before are younger than the loads of the first stages
-        if (stored) __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads + kStores>::value);
-        else __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads>::value);
-        lds_barrier();
+      if constexpr (q == 1) loads = next_loads(spent);
+      if constexpr (q == C::kFragK - 1) {
+        if (barrier) {
+          // stores of the tile before may be younger than the loads waited for
+          if (__builtin_expect(stored, 0)) __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads + kStores>::value);
+          else __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<kAhead * C::kLoads>::value);
+          lds_barrier();
+        }
       }
       static_for<0, C::kLoads + 1>([&](auto l) {
         if constexpr (q == C::kFragK + 1 + l * ((kSlots - C::kFragK) / (C::kLoads + 1))) load_piece(loads, l);
@@ -340,15 +383,15 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
       if constexpr (q >= C::kFragK && q < C::kFragK + kReads) read_right(stage, raw, q - C::kFragK);
       static_for<0, C::kFragN - 1>([&](auto f) {
         constexpr int at = (f + 1) * C::kFragK + (f == 0 ? 4 : f == 1 ? 2 : 0);
-        if constexpr (q == at || q == at + 1) read16(stage + at_n[f], C::kPitchN, fn[f], q - at);
+        if constexpr (q == at || q == at + 1) read16(stage + an[f], C::kPitchN, fn[f], q - at);
       });
       if constexpr (q >= kConvert)
         static_for<(q - kConvert) * kPieces / (kSlots - kConvert), (q + 1 - kConvert) * kPieces / (kSlots - kConvert)>(
             [&](auto piece) { convert(raw, next, piece); });
       __builtin_amdgcn_sched_barrier(0);
     });
-    read16(stage + at_n[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 0);
-    read16(stage + at_n[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 1);
+    read16(stage + an[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 0);
+    read16(stage + an[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 1);
   };
 
   // Writes a tile; true if that took kStores stores and no loads.
@@ -404,68 +447,68 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     return inside;
   };
 
-  const int grid = (int)gridDim.x;   // a multiple of 8
-  const int mine = (int)(blockIdx.x & 7) * (grid >> 3) + (int)(blockIdx.x >> 3);
-  // unit of a round: forwards and backwards in turn, so that who gets the longest of one gets the shortest
-  // of the next (groups come in order of their rows)
-  auto unit_in = [&](int round) { return round * grid + (round & 1 ? grid - 1 - mine : mine); };
-  int round = 0, u = unit_in(0);
-  if (u >= units) return;
-  Unit w = unit_of(u);
-  begin(w);
-  for (int s = 0; s < kBegun; ++s) load_stage(s);
-  bool stored = false;
-  while (true) {
+  Right even, odd;
+  int before = 0, buffer = 0;   // of the stage before and of the present one
+  bool first = true;            // of a pair, which has the barrier
+  auto after = [](int b) { return b + 1 == C::kStages ? 0 : b + 1; };
+  // The first loads, and the first stage's fragments.
+  auto fill = [&]() {
+#pragma unroll 1
+    for (int s = 0; s < kBegun; ++s) load_stage(s);
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(kBegun - 1) * C::kLoads>::value);
+    lds_barrier();
+    Raw raw;
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) read_right(base, raw, i);
+#pragma unroll
+    for (int i = 0; i < 2 * C::kFragN; ++i) read16(base + an[i >> 1], C::kPitchN, fn[i >> 1], i & 1);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) convert(raw, even, i);
+    before = C::kStages - 1;
+    buffer = 0;
+    first = true;
+  };
+  // Steps since a tile's stores.  A barrier waits for loads that were issued kStages - 3 (pairs) or kStages - 1
+  // steps earlier: until that many steps later they are older than the stores.
+  constexpr int kGrace = C::kPairs ? C::kStages - 3 : C::kStages - 1;
+  int since = kGrace;
+  auto next_step = [&](const Right& now, Right& next) {
+    const int to = after(buffer);
+    step(!C::kPairs || first, now, next, C::kPairs ? before : buffer, to, ++since <= kGrace);
+    before = buffer;
+    buffer = to;
+    first = !first;
+  };
+  Unit w = unit_of(unit_in(0));
+  if constexpr (C::kAcross) fill();
+  for (int round = 0;;) {
+    if constexpr (!C::kAcross) {
+      begin(w);
+      fill();
+    }
 #pragma unroll
     for (int i = 0; i < C::kFragN; ++i)
 #pragma unroll
       for (int j = 0; j < C::kFragK; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    if (w.stages > 0) {
-      Right even, odd;
-      if (stored) __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(kBegun - 1) * C::kLoads + kStores>::value);
-      else __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<(kBegun - 1) * C::kLoads>::value);
+    // one way out of the loop: with two the compiler gives each its own registers for the sums
+    for (int s = 0; s < w.stages; s += 2) {
+      next_step(even, odd);
+      if (s + 1 < w.stages) next_step(odd, even);
+      else even = odd;
+    }
+    const bool counted = put(w);
+    since = C::kAcross && counted ? 0 : kGrace;
+    const int u = unit_in(++round);
+    if (u >= units) break;   // only the last round is not whole
+    w = unit_of(u);
+    if constexpr (!C::kAcross) {
+      // nothing may be on its way to LDS, nor be read there, when the next tile's loads begin
+      __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
       lds_barrier();
-      {
-        Raw raw;
-#pragma unroll
-        for (int i = 0; i < kReads; ++i) read_right(base, raw, i);
-#pragma unroll
-        for (int i = 0; i < 2 * C::kFragN; ++i) read16(base + at_n[i >> 1], C::kPitchN, fn[i >> 1], i & 1);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) convert(raw, even, i);
-      }
-      int before = C::kStages - 1, buffer = 0;   // of the stage before and of this one
-      auto after = [](int b) { return b + 1 == C::kStages ? 0 : b + 1; };
-      // stores are younger than the loads of stages 0 .. kBegun - 1; barriers of pairs wait for every other stage
-      int grace = stored ? (C::kPairs ? (kBegun - 1) / 2 : kBegun - 1) : 0;
-      for (int s = 0;;) {
-        int to = after(buffer);
-        step(std::true_type{}, even, odd, C::kPairs ? before : buffer, to, grace-- > 0);
-        before = buffer;
-        buffer = to;
-        if (++s == w.stages) break;
-        to = after(buffer);
-        if constexpr (C::kPairs) step(std::false_type{}, odd, even, before, to, false);
-        else step(std::true_type{}, odd, even, buffer, to, grace-- > 0);
-        before = buffer;
-        buffer = to;
-        if (++s == w.stages) break;
-      }
     }
-    // nothing may be on its way to LDS, nor be read there, when the next tile's loads begin
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
-    lds_barrier();
-    const Unit last = w;
-    u = unit_in(++round);
-    const bool more = u < units;   // only the last round is not whole
-    if (more) {
-      w = unit_of(u);
-      begin(w);
-      for (int s = 0; s < kBegun; ++s) load_stage(s);
-    }
-    stored = put(last);
-    if (!more) break;
   }
+  // no load may be on its way to LDS when the workgroup ends
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm0<0>::value);
 }
 
 // dW from the partial sums of the splits, in their order; four columns a thread.

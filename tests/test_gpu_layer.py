@@ -86,7 +86,7 @@ def near_codes(q, sf, want, err, ue8m0=False, what=""):
 # ---------------------------------------------------------------- norm
 
 NORM_SHAPES = [(1, 8), (1, 7168), (2, 128), (5, 512), (3, 520), (7, 1024), (4, 1032), (33, 2048), (9, 2056), (5, 4096),
-               (6, 4104), (3, 8192), (2, 8200), (3, 16384), (17, 16376), (1025, 256)]
+               (6, 4104), (3, 8192), (2, 8200), (3, 16384), (17, 16376), (1025, 256), (300, 4104), (257, 2056)]
 
 
 def norm_inputs(m, k, dtype, seed, residual=True):
@@ -140,7 +140,7 @@ def test_norm_in_place_and_outputs_that_are_given():
 
 
 @pytest.mark.parametrize("m,k", [(1, 128), (1, 7168), (5, 512), (3, 640), (33, 1024), (4, 1152), (9, 2176), (3, 4096),
-                                 (2, 8192), (2, 8320), (3, 16384), (600, 256)])
+                                 (2, 8192), (2, 8320), (3, 16384), (600, 256), (260, 4224), (258, 8320)])
 @pytest.mark.parametrize("ue8m0", [False, True])
 def test_norm_cast_fp8(m, k, ue8m0):
     """fp32 rows: the codes are those of the cast of the rows that the same call returns, bit for bit; 16-bit rows: within
@@ -162,7 +162,7 @@ def test_norm_cast_fp8(m, k, ue8m0):
 
 
 @pytest.mark.parametrize("m,k", [(1, 16), (1, 7168), (5, 528), (33, 1024), (4, 1040), (9, 2176), (3, 7152), (2, 8208),
-                                 (3, 16384)])
+                                 (3, 16384), (257, 4112), (259, 2064)])
 def test_norm_cast_int8(m, k):
     x, r, w, h = norm_inputs(m, k, F32, 7 * m + k)
     y = torch.empty((m, k), device=device())
@@ -292,6 +292,10 @@ def layout_of(kind, m, seed):
     return {"masked_m": torch.from_numpy(count).to(device())}, valid
 
 
+def raw(t):
+    return t.view(torch.uint8) if t.dtype == FP8 else t
+
+
 def sentinel(shape):
     return torch.full(shape, 0x7D, dtype=torch.uint8, device=device())
 
@@ -364,6 +368,36 @@ def test_swiglu_grad(m, n, kind, dtype):
             if dtype is F32:
                 oq, osf = quant.per_token_cast(dh[valid].cpu().numpy())
                 assert np.array_equal(codes(q)[valid], oq) and np.array_equal(gs.cpu().numpy()[valid], osf)
+
+
+@pytest.mark.parametrize("saved", ["rows", "codes"])
+def test_swiglu_of_many_rows(saved):
+    """2^24 elements and more: threads take two pieces each.  The same rows in batches of 100 give the same bits, and
+    those are compared with the formulas above."""
+    m, n, part = 8400, 2176, 100
+    h, da = (rows((m, w), BF16, 4 + w, 0.0).to(device()) for w in (2 * n, n))
+    mi = torch.randint(-1, 3, (m,), dtype=torch.int32, device=device())
+    for where in ({}, {"m_indices": mi}, {"masked_m": torch.tensor([0, 5, 1400, 699, 1, 1300], dtype=torch.int32,
+                                                                   device=device())}):
+        valid = torch.ones(m, dtype=torch.bool, device=device())
+        if "m_indices" in where:
+            valid = mi >= 0
+        if "masked_m" in where:
+            valid = (torch.arange(m // 6, device=device())[None] < where["masked_m"][:, None]).reshape(-1)
+        q, hq = sentinel((m, n)), sentinel((m, 2 * n))
+        (_, sf), (_, hs) = dg.swiglu_checkpoint_fp8(h, **where, q=q, hq=hq)
+        dq, given = sentinel((m, 2 * n)), h
+        if saved == "codes":
+            given = dg.swiglu_checkpoint_fp8(h)[1]
+        dh, (_, ds) = dg.swiglu_grad_cast_fp8(da, given, **where, q=dq)
+        for i in range(0, m, part):
+            s, v = slice(i, i + part), valid[i:i + part]
+            (q2, sf2), (hq2, hs2) = dg.swiglu_checkpoint_fp8(h[s])
+            piece = tuple(t[s] for t in given) if saved == "codes" else given[s]
+            dh2, (dq2, ds2) = dg.swiglu_grad_cast_fp8(da[s], piece)
+            for a, b in ((q, q2), (hq, hq2), (dq, dq2), (sf, sf2), (hs, hs2), (ds, ds2), (dh, dh2)):
+                assert torch.equal(raw(a[s])[v], raw(b)[v])
+            assert bool((q[s][~v] == 0x7D).all()) and bool((hq[s][~v] == 0x7D).all()) and bool((dq[s][~v] == 0x7D).all())
 
 
 def test_swiglu_grad_in_place():
@@ -450,7 +484,8 @@ def test_weight_grad(m, n, k, out):
 
 GROUPS = [([5], 1, 200, 136), ([0, 3, 0, 130, 1, 64], 128, 64, 256), ([0, 3, 0, 130, 1, 64], 1, 64, 256),
           ([129, 0, 0, 257], 128, 264, 128), ([1] * 40, 1, 128, 128), ([7, 65, 300, 12], 32, 512, 384),
-          ([0, 0], 1, 128, 128), ([40, -3, 9], 128, 8, 128), ([64] * 3, 1, 2048, 4096)]
+          ([0, 0], 1, 128, 128), ([40, -3, 9], 128, 8, 128), ([64] * 3, 1, 2048, 4096),
+          ([0, 1, 33, 70, 0, 200, 32, 64, 31, 0] * 14, 1, 264, 136), ([0] * 300 + [9] + [0] * 20 + [130], 1, 40, 128)]
 
 
 @pytest.mark.parametrize("i", range(len(GROUPS)))
@@ -507,6 +542,63 @@ def test_weight_grad_masked(groups, max_m, n, k, fp8):
     dg.m_grouped_weight_grad_masked(dy.to(device()), given, dw,
                                     torch.from_numpy(count.astype(np.int32)).to(device()))
     check_weight_grad(dw, dy, value, segs, F32, False)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_weight_grad_is_the_same_on_few_cus(fp8, out):
+    """Fewer workgroups take more tiles each, in the same way."""
+    shapes = (([70, 0, 33, 1, 300, 64] * 12, 520, 384), ([700, 12], 264, 256))
+    for count, n, k in shapes:
+        total = sum(count)
+        dy, x = rows((total, n), BF16, n), rows((total, k), BF16, k)
+        given, value = kept_rows(x, True) if fp8 else (x.to(device()), f64(x))
+        counts = torch.tensor(count, dtype=torch.int32, device=device())
+        got = []
+        cus = dg.get_num_cus()
+        for few in (cus, 8, 24, 1):
+            dg.set_num_cus(few)
+            try:
+                dw = torch.empty((len(count), n, k), dtype=out, device=device())
+                dg.m_grouped_weight_grad_contiguous(dy.to(device()), given, dw, counts, alignment=1)
+            finally:
+                dg.set_num_cus(cus)
+            got.append(dw)
+        assert all(torch.equal(got[0], g) for g in got[1:])
+        check_weight_grad(got[0], dy, value, layer.segments(count, total, 1), out, False)
+
+
+def test_operands_of_more_than_2_to_the_32_bytes():
+    """Rows that lie 2^16 elements apart: offsets pass 32 bits.  What they hold is compared with the same
+    rows side by side."""
+    m, n, k = 33000, 264, 256
+    dy, x = rows((m, n), BF16, 1, 0.0).to(device()), rows((m, k), BF16, 2, 0.0).to(device())
+    wide = torch.empty((m, 65536), dtype=BF16, device=device())
+    for count in ([m - 200, 0, 77, 123], [1, 2, 0, m - 3] * 9):
+        counts = torch.tensor(count, dtype=torch.int32, device=device())
+        total = min(m, sum(count))
+        wide[:, :k], wide[:, k:k + n] = x, dy
+        want, got = (torch.empty((len(count), n, k), device=device()) for _ in range(2))
+        dg.m_grouped_weight_grad_contiguous(dy, x, want, counts, alignment=1)
+        dg.m_grouped_weight_grad_contiguous(wide[:, k:k + n], wide[:, :k], got, counts, alignment=1)
+        assert torch.equal(got, want) and bool(want[0].any())
+    w = torch.rand(k, device=device())
+    y, h, rstd = dg.rms_norm(x, w)
+    wide[:, k:2 * k] = x
+    _, gh, gr = dg.rms_norm(wide[:, k:2 * k], w, y=wide[:, :k], h=wide[:, 2 * k:3 * k])
+    assert torch.equal(wide[:, :k], y) and torch.equal(gh, h) and torch.equal(gr, rstd)
+    dx, dw = dg.rms_norm_grad(y, x, w, rstd, x)
+    gx, gw = dg.rms_norm_grad(wide[:, :k], wide[:, k:2 * k], w, rstd, wide[:, 2 * k:3 * k], dx=wide[:, 3 * k:4 * k])
+    assert torch.equal(gx, dx) and torch.equal(gw, dw)
+    (q, sf), (hq, hs) = dg.swiglu_checkpoint_fp8(x)
+    bytes_ = wide.view(torch.uint8)
+    at = 65536
+    (q2, sf2), (hq2, hs2) = dg.swiglu_checkpoint_fp8(wide[:, k:2 * k], q=bytes_[:, at:at + k // 2], hq=bytes_[:, at + k:at + 2 * k])
+    for a, b in ((q, q2), (sf, sf2), (hq, hq2), (hs, hs2)):
+        assert torch.equal(raw(a), raw(b))
+    da = dy[:, :k // 2]
+    assert torch.equal(dg.swiglu_grad(da, x), dg.swiglu_grad(da, wide[:, k:2 * k], dh=wide[:, 4 * k:5 * k]))
+    assert torch.equal(dg.swiglu_grad(da, (hq, hs)), dg.swiglu_grad(da, (hq2, hs2), dh=wide[:, 4 * k:5 * k]))
 
 
 def test_weight_grad_without_rows_or_columns():
