@@ -2,13 +2,15 @@
 
     python examples/moe_layer.py [--int8] [--decode] [--train] [--tokens T] [--experts E] [--hidden H] [--inner I]
 
-Router logits -> route_topk -> expert layout -> dispatch with the cast -> grouped product (gate and up) -> SiLU ->
-cast -> grouped product (down) -> combine.  Nothing in the layer reads the routing on the host.
+Residual and norm -> router logits -> route_topk -> expert layout -> dispatch with the cast -> grouped product (gate and
+up) -> gated activation with the cast -> grouped product (down) -> combine.  Nothing in the layer reads the routing on
+the host.
 
 * prefill (default): contiguous layout, experts' rows padded to 128;
 * --decode: masked layout, a fixed number of rows for each expert, for few tokens;
 * --int8: experts in 8-bit integers with scales per token and channel, instead of FP8 with block scales;
-* --train: also the gradient that reaches the router's logits, through combine_grad and route_topk_grad.
+* --train: also the gradient that reaches the router's logits, through combine_grad and route_topk_grad; with FP8 all of
+  the layer's gradients, from what the forward pass keeps in 8 bits: the experts' weights', the norm's, and the input's.
 """
 import argparse
 import os
@@ -25,11 +27,14 @@ ROUTE = dict(score="sigmoid", num_expert_groups=4, topk_groups=2, group_score="t
 
 
 class Experts:
-    """Weights of all experts, laid out once: [E, 2 * inner, hidden] and [E, hidden, inner] in 8 bits."""
+    """Weights of all experts, laid out once: [E, 2 * inner, hidden] and [E, hidden, inner] in 8 bits, and transposed for
+    the way back."""
 
-    def __init__(self, up: torch.Tensor, down: torch.Tensor, int8: bool):
+    def __init__(self, up: torch.Tensor, down: torch.Tensor, int8: bool, train: bool = False):
         self.int8 = int8
         self.up, self.down = self._cast(up), self._cast(down)
+        if train:
+            self.up_t, self.down_t = (self._cast(w.transpose(1, 2).contiguous()) for w in (up, down))
 
     def _cast(self, w: torch.Tensor):
         pairs = [dg.per_token_cast_int8(x) if self.int8 else dg.per_block_cast_fp8(x) for x in w]
@@ -41,6 +46,13 @@ class Experts:
     def dispatch(self, x: torch.Tensor, layout: dg.ExpertLayout):
         f = dg.dispatch_cast_int8 if self.int8 else dg.dispatch_cast_fp8
         return f(x, layout.slot_row, rows=layout.rows)
+
+    def activation(self, h: torch.Tensor, layout: dg.ExpertLayout, max_m: int, keep: bool):
+        """The second product's operand, and h in 8 bits if it is kept."""
+        where = rows_of(layout, max_m)
+        if keep:
+            return dg.swiglu_checkpoint_fp8(h, **where)
+        return (dg.swiglu_cast_int8 if self.int8 else dg.swiglu_cast_fp8)(h, **where), None
 
     def product(self, a, w, layout: dg.ExpertLayout, max_m: int) -> torch.Tensor:
         """[rows, n]; rows that hold no token are unspecified."""
@@ -55,27 +67,72 @@ class Experts:
         return d
 
 
-def moe_layer(x, logits, bias, experts: Experts, topk: int, max_m: int = 0):
-    """out [tokens, hidden], and what the backward pass needs.  max_m > 0: masked layout of that many rows per expert."""
+def rows_of(layout: dg.ExpertLayout, max_m: int) -> dict:
+    """The rows that hold a token, as the activation takes them."""
+    return {"masked_m": layout.counts} if max_m else {"m_indices": layout.m_indices}
+
+
+def moe_layer(x, logits, bias, experts: Experts, topk: int, max_m: int = 0, keep: bool = False):
+    """out [tokens, hidden], and what the backward pass needs (``keep``: for the experts' gradients too).  max_m > 0:
+    masked layout of that many rows per expert."""
     indices, weights = dg.route_topk(logits, topk, bias=bias, **ROUTE)
     num_experts = logits.shape[1]
     layout = (dg.expert_layout_masked(indices, num_experts, max_m) if max_m
               else dg.expert_layout_contiguous(indices, num_experts))
-    h = experts.product(experts.dispatch(x, layout), experts.up, layout, max_m)
-    gate, up = h.chunk(2, dim=1)
-    y = experts.product(experts.cast(torch.nn.functional.silu(gate) * up), experts.down, layout, max_m)
-    return dg.combine(y, layout.slot_row, weights), (indices, weights, layout, y)
+    a = experts.dispatch(x, layout)
+    h = experts.product(a, experts.up, layout, max_m)
+    act, kept = experts.activation(h, layout, max_m, keep)
+    y = experts.product(act, experts.down, layout, max_m)
+    return dg.combine(y, layout.slot_row, weights), (indices, weights, layout, y) + ((a, act, kept) if keep else ())
 
 
 def router_grad(dout, logits, saved):
     """Gradient of the loss with respect to the router's logits, the experts' outputs held fixed."""
-    indices, weights, layout, y = saved
+    indices, weights, layout, y = saved[:4]
     _, dweights = dg.combine_grad(dout, y, layout.slot_row, layout.row_slot, weights)
     return dg.route_topk_grad(logits, indices, dweights, score=ROUTE["score"], scale=ROUTE["scale"])
 
 
+def experts_grad(dout, saved, experts: Experts, max_m: int = 0):
+    """Gradients of the experts' weights, fp32 [E, 2 * inner, hidden] and [E, hidden, inner], and of the layer's input by
+    way of the experts."""
+    _, weights, layout, y, a, act, kept = saved
+    drows, _ = dg.combine_grad(dout, y, layout.slot_row, layout.row_slot, weights)
+    weight_grad = dg.m_grouped_weight_grad_masked if max_m else dg.m_grouped_weight_grad_contiguous
+    d_up, d_down = (torch.empty(w[0].shape, dtype=torch.float32, device=dout.device)
+                    for w in (experts.up, experts.down))
+    weight_grad(drows, act, d_down, layout.counts)
+    dact = experts.product(experts.cast(drows), experts.down_t, layout, max_m)
+    dh, carried = dg.swiglu_grad_cast_fp8(dact, kept, **rows_of(layout, max_m))
+    weight_grad(dh, a, d_up, layout.counts)
+    dx_rows = experts.product(carried, experts.up_t, layout, max_m)
+    return d_up, d_down, dg.combine(dx_rows, layout.slot_row)
+
+
+class Block:
+    """x + residual -> h; h + experts(norm(h)): a layer of the model, forwards and backwards."""
+
+    def __init__(self, norm, router, bias, experts: Experts, topk: int, max_m: int = 0):
+        self.norm, self.router, self.bias, self.experts, self.topk, self.max_m = norm, router, bias, experts, topk, max_m
+
+    def forward(self, x, residual, keep: bool = False):
+        y, h, rstd = dg.rms_norm(x, self.norm, residual)
+        logits = y.float() @ self.router.t()
+        out, saved = moe_layer(y, logits, self.bias, self.experts, self.topk, self.max_m, keep)
+        return h + out, (y, h, rstd, logits, saved)
+
+    def backward(self, dout, kept) -> dict:
+        """Gradients of up, down, router, norm and x (the residual's is x's), for that of the output."""
+        y, h, rstd, logits, saved = kept
+        d_up, d_down, dy = experts_grad(dout, saved, self.experts, self.max_m)
+        dlogits = router_grad(dout, logits, saved)
+        dy = (dy.float() + dlogits @ self.router).to(dout.dtype)
+        dx, d_norm = dg.rms_norm_grad(dy, h, self.norm, rstd, dout)
+        return dict(up=d_up, down=d_down, router=dlogits.t() @ y.float(), norm=d_norm, x=dx)
+
+
 def plain_layer(x, logits, indices, up, down):
-    """The layer in fp32 for a given choice of experts, differentiable in the logits: (out, experts' rows per slot)."""
+    """The layer in fp32 for a given choice of experts, differentiable: (out, experts' rows per slot)."""
     s = torch.sigmoid(logits).gather(1, indices.long())
     w = ROUTE["scale"] * s / s.sum(1, keepdim=True)
     rows = torch.zeros(indices.shape + (x.shape[1],), device=x.device)
@@ -85,6 +142,17 @@ def plain_layer(x, logits, indices, up, down):
             gate, u = (x[t].float() @ up[e].t()).chunk(2, dim=1)
             rows[t, j] = (torch.nn.functional.silu(gate) * u) @ down[e].t()
     return (w[..., None] * rows).sum(1), rows
+
+
+def plain_grads(x, residual, dout, indices, norm, router, up, down, eps: float = 1e-6) -> dict:
+    """The block's gradients in fp32, for a given choice of experts."""
+    leaves = dict(up=up, down=down, router=router, norm=norm, x=(x + residual).float())
+    leaves = {k: v.detach().clone().requires_grad_() for k, v in leaves.items()}
+    h = leaves["x"]
+    y = h * (h.square().mean(1, keepdim=True) + eps) ** -0.5 * leaves["norm"]
+    out, _ = plain_layer(y, y @ leaves["router"].t(), indices, leaves["up"], leaves["down"])
+    ((h + out) * dout.float()).sum().backward()
+    return {k: v.grad for k, v in leaves.items()}
 
 
 def main(argv=None) -> dict:
@@ -105,7 +173,8 @@ def main(argv=None) -> dict:
     bias = torch.randn(a.experts, generator=g, device="cuda") * 0.05
     up = torch.randn((a.experts, 2 * a.inner, a.hidden), generator=g, device="cuda") * a.hidden ** -0.5
     down = torch.randn((a.experts, a.hidden, a.inner), generator=g, device="cuda") * a.inner ** -0.5
-    experts = Experts(up, down, a.int8)
+    train = a.train and not a.int8
+    experts = Experts(up, down, a.int8, train)
     max_m = min(256, -(-tokens // 8) * 8) if a.decode else 0
     logits = x.float() @ router.t()
 
@@ -121,10 +190,21 @@ def main(argv=None) -> dict:
         got = router_grad(dout, logits, saved)
         found["dlogits"] = float((got - leaf.grad).norm() / leaf.grad.norm())
 
+    norm = torch.rand(a.hidden, generator=g, device="cuda") + 0.5
+    residual = torch.randn(x.shape, generator=g, device="cuda").to(torch.bfloat16)
+    block = Block(norm, router, bias, experts, a.topk, max_m)
+    if train:
+        _, kept = block.forward(x, residual, keep=True)
+        got = block.backward(dout, kept)
+        for name, w in plain_grads(x, residual, dout, kept[4][0], norm, router, up, down).items():
+            found["d" + name] = float((got[name].float() - w).norm() / w.norm())
+
     torch.cuda.synchronize()
     begun, passes = time.perf_counter(), 20
     for _ in range(passes):
-        moe_layer(x, logits, bias, experts, a.topk, max_m)
+        _, kept = block.forward(x, residual, keep=train)
+        if train:
+            block.backward(dout, kept)
     torch.cuda.synchronize()
     found["us"] = (time.perf_counter() - begun) / passes * 1e6
     print(f"{'int8' if a.int8 else 'fp8'} {'masked' if a.decode else 'contiguous'}, {tokens} tokens, top {a.topk} of "
