@@ -730,8 +730,8 @@ dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t 
  * h and y may be x or residual (same address and stride), not each other.  An element past
  * 1.8e19 overflows its square: rstd is 0 then.  A NaN or an infinity makes its row NaN
  * (where it is finite, 0).
- * Limits: k % 8 == 0, k <= 16384, rows <= 2^23 -> otherwise DG_ERROR_NOT_SUPPORTED, as for
- * misaligned rows.
+ * Limits: k % 8 == 0, k <= 16384, rows <= 2^23 (2^21 where k > 8192) -> otherwise
+ * DG_ERROR_NOT_SUPPORTED, as for misaligned rows.
  */
 dg_status dg_rms_norm(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, int weight_dtype, float eps, void* h, int64_t ldh,
@@ -832,7 +832,7 @@ dg_status dg_swiglu_grad(const void* da, int dtype, int64_t ldda, const void* h,
  *   ws        device, 16-byte aligned, dg_weight_grad_workspace_size() bytes (contents do not
  *             matter): lets several workgroups share a tile's rows where there are few tiles; NULL
  *             or smaller: they do not.  Calls that may overlap need distinct ones
- * Sums are fp32, in an order that the sizes alone give.
+ * Sums are fp32, in an order that the sizes, num_groups and whether ws is there alone give.
  * Limits: n % 8 == 0, k % 8 == 0 (codes: k % 128 == 0), n, k, lddy, ldx, sf_sm < 2^24, rows < 2^31, rows of
  * dy, x and dw at 16-byte boundaries -> otherwise DG_ERROR_NOT_SUPPORTED.  rows == 0 gives zeros.
  */

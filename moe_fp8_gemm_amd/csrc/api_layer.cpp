@@ -12,7 +12,10 @@
 namespace dgfp8 {
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 23;         // a workgroup per row: grid x block inside 32 bits
+// A workgroup a row: grid x block inside 32 bits, for 256 lanes and for the norm's 1024.
+constexpr int64_t kMaxRows = (int64_t)1 << 23;
+constexpr int64_t kMaxWideRows = (int64_t)1 << 21;
+constexpr int64_t kWide = 8192;                        // columns
 constexpr int64_t kMaxInner = (int64_t)1 << 24;
 constexpr int64_t kMaxInnerInt8 = 16384;               // a row's results in registers
 constexpr int64_t kMaxLd = ((int64_t)1 << 24) - 1;     // weights' gradients: 32 rows inside 2^31 bytes
@@ -31,7 +34,8 @@ dg_status check_norm(int dtype, int64_t rows, int64_t k) {
   return DG_SUCCESS;
 }
 dg_status check_width(int64_t rows, int64_t k) {
-  return k % 8 != 0 || k > kMaxNormWidth || rows > kMaxRows ? DG_ERROR_NOT_SUPPORTED : DG_SUCCESS;
+  return k % 8 != 0 || k > kMaxNormWidth || rows > (k > kWide ? kMaxWideRows : kMaxRows) ? DG_ERROR_NOT_SUPPORTED
+                                                                                         : DG_SUCCESS;
 }
 
 // Everything but the quantized output.  launch: whether there is anything to do.

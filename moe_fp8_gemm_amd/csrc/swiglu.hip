@@ -10,8 +10,14 @@
 // left out, so that its relative error is a few units of the last place at any g.
 //
 // Bound by memory: each element is read once and written once, in 16-byte pieces (8 bytes of
-// codes).  A layout's rows without a token are skipped: m_indices marks them row by row,
-// masked_m ends a group's rows early.
+// codes), past L2.  A layout's rows without a token are skipped: m_indices marks them row by row,
+// masked_m ends a group's rows early.  Measured, bf16: 32768 tokens' rows of 2 x 2048 among 256 experts' padding, with
+// the checkpoint (476 MB) 102 us, 4.7 TB/s; the gradient from the checkpoint with its cast (680 MB) 131 us, 5.2 TB/s;
+// 16 x 256 rows with at most 32 tokens each 4.7 us, 333 rows' gradient 4.2, of which a launch that does nothing has 3.6.
+//
+// Tried: rows in a run for each XCD's L2 155 and 170 us; 16 elements a thread side by side 135 and 191; codes
+// written through the caches 102 and 133; the sigmoid without what the rounding of g log2 e left out: 3 us less, twice as many
+// codes beside the exact value's.
 #include "cast_rules.h"
 #include "elem_types.h"
 #include "layer_internal.h"
@@ -275,7 +281,8 @@ dim3 grid_of(const RowSet& at, int64_t items, int64_t per_block) {
   return dim3((unsigned)x, (unsigned)at.groups);
 }
 
-// Blocks of 128 columns that a workgroup takes at once.
+// Blocks of 128 columns that a workgroup takes at once, where there are workgroups enough: 32768 rows of 2 x 2048, with
+// the checkpoint and its gradient: 1 110 and 136 us, 2 99 and 127, 4 98 and 139, 8 112 and 148.
 constexpr int kMany = 2;
 bool many_blocks(const RowSet& at, int64_t inner) { return at.group_rows * at.groups * inner >= (int64_t)1 << 24; }
 dim3 block_grid(const RowSet& at, int64_t inner, int at_once) {

@@ -27,6 +27,7 @@ NORM_CASES = [
     (dict(residual=P + 8), UNSUPPORTED), (dict(weight=P + 2), UNSUPPORTED), (dict(rstd=P + 2), UNSUPPORTED),
     (dict(ldx=260), UNSUPPORTED), (dict(ldr=1 << 41), UNSUPPORTED), (dict(k=252), UNSUPPORTED),
     (dict(rows=(1 << 23) + 1), UNSUPPORTED),
+    (dict(rows=(1 << 21) + 1, k=8448, ldx=8448, ldr=8448, ldh=8448, ldy=8448), UNSUPPORTED),
     (dict(k=16392, ldx=16392, ldr=16392, ldh=16392, ldy=16392), UNSUPPORTED)]
 
 
