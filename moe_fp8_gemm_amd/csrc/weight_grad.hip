@@ -21,10 +21,11 @@
 //
 // Bound by matrix instructions, at the clock that the card's power leaves them (1.9 to 2.2 GHz), where groups have
 // many rows, and by the operands' and dW's way through memory where they have few.  Measured, with operands that no
-// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 577 us with fp32 sums (835 TFLOP/s, 940 MB of dW) and
-// 488 us in bf16 (985), 16-bit rows 570 and 466 us; 64 experts, 16384 rows, 2048 x 1408: codes 257 and 172 us
-// (738 MB of fp32, 369 of bf16), 16-bit rows 281 and 189 us; a dense 8191 x 512 x 2176 in 34 us.
-// Each tile with a prologue of its own: 600 and 507, 260 and 199 us (codes).
+// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 521 us with fp32 sums (923 TFLOP/s, 940 MB of dW) and
+// 459 us in bf16 (1048), 16-bit rows 507 and 436 us; 64 experts, 16384 rows, 2048 x 1408: codes 209 and 156 us
+// (738 MB of fp32, 369 of bf16), 16-bit rows 221 and 160 us; a dense 8191 x 512 x 2176 in 33 us.
+// Before dW went out in whole lines 576 and 484, 258 and 172 us (codes): half lines reached memory 1.46 times.  Before
+// that, with a prologue for each tile, 600 and 507, 260 and 199 us.
 //
 // Tried: the 32 x 32 x 16 instruction takes 11% fewer cycles a stage, and the clock falls by 14%; two workgroups of
 // 256 x 128 a CU 977 TFLOP/s where one of 256 x 256 does 1062 (4096^3, 16-bit rows 1014 and 1173).
@@ -394,24 +395,43 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     read16(stage + an[C::kFragN - 1], C::kPitchN, fn[C::kFragN - 1], 1);
   };
 
-  // Writes a tile; true if that took kStores stores and no loads.
+  // Writes a tile; true if that took kStores stores and no loads.  Lanes 8 apart exchange halves of what two neighbouring
+  // stores write, so that each writes whole 128-byte lines of 8 rows, not half lines of 16.
+  auto halves = [&](uint32_t& a, uint32_t& b) {
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(lane & 8 ? a : b), 0x128 /* row_ror:8 */, 0xF, 0xF, true);
+    if (lane & 8) a = other;
+    else b = other;
+  };
   auto put = [&](const Unit& w) -> bool {
     const bool inside = w.n0 + C::kTn <= p.n && w.k0 + C::kTk <= p.k;
-    const int64_t n0 = w.n0 + wn * C::kFragN * 16 + (lane & 15), k0 = w.k0 + wk * C::kFragK * 16;
+    const int64_t n0 = w.n0 + wn * C::kFragN * 16 + (lane & 7), k0 = w.k0 + wk * C::kFragK * 16;
+    const int upper = (lane >> 3) & 1;
     if (kF32 || p.splits > 1) {
-      // lane: row n = lane % 16 of fragment i, columns k = 4 (lane / 16) .. of fragment j
+      // lane: row n = lane % 16 of fragment i, columns k = 4 (lane / 16) .. of fragment j; then rows lane % 8 and + 8 of
+      // fragment j or j + 1
       float* dw = p.splits > 1 ? p.partial + ((int64_t)w.split * p.groups + w.g) * p.n * p.k
                                : (float*)p.dw + w.g * p.dw_gs;
-      const int64_t ld = p.splits > 1 ? p.k : p.lddw, k1 = k0 + (lane >> 4) * 4;
+      const int64_t ld = p.splits > 1 ? p.k : p.lddw, k1 = k0 + upper * 16 + (lane >> 4) * 4;
       const bool add = p.accumulate && p.splits == 1;
       auto each = [&](auto&& f) {
 #pragma unroll
         for (int i = 0; i < C::kFragN; ++i) {
           float* row = dw + (n0 + i * 16) * ld + k1;
 #pragma unroll
-          for (int j = 0; j < C::kFragK; ++j)
+          for (int j = 0; j < C::kFragK; j += 2) {
+            u32x4 a = __builtin_bit_cast(u32x4, acc[i][j]), b = __builtin_bit_cast(u32x4, acc[i][j + 1]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t x = a[h], y = b[h];
+              halves(x, y);
+              a[h] = x;
+              b[h] = y;
+            }
             // k is a multiple of 8: four columns are in or out together
-            if (inside || (n0 + i * 16 < p.n && k1 + j * 16 < p.k)) f((f32x4*)(row + j * 16), acc[i][j]);
+            const bool in = inside || k1 + j * 16 < p.k;
+            if (inside || (in && n0 + i * 16 < p.n)) f((f32x4*)(row + j * 16), __builtin_bit_cast(f32x4, a));
+            if (inside || (in && n0 + i * 16 + 8 < p.n)) f((f32x4*)(row + 8 * ld + j * 16), __builtin_bit_cast(f32x4, b));
+          }
           __builtin_amdgcn_sched_barrier(0);   // no more than a row's addresses and sums at once
         }
       };
@@ -422,26 +442,34 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
       return inside && !add && kF32;
     }
     // Two fragments side by side: lanes 16 apart exchange halves, so that each has eight columns in a row:
-    // 16 (lane / 16 % 2) + 8 (lane / 32) ..
+    // 16 (lane / 16 % 2) + 8 (lane / 32) ..; then, as above, of the first two fragments or of the last
     uint16_t* dw = (uint16_t*)p.dw + w.g * p.dw_gs;
-    const int64_t k1 = k0 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+    const int64_t k1 = k0 + upper * 32 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+    static_assert(C::kFragK == 4, "two stores of two fragments");
 #pragma unroll
     for (int i = 0; i < C::kFragN; ++i) {
       uint16_t* row = dw + (n0 + i * 16) * p.lddw + k1;
+      u32x4 v[2];
 #pragma unroll
-      for (int j = 0; j < C::kFragK; j += 2) {
-        u32x4 v;
+      for (int j = 0; j < 4; j += 2) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t a = pack_bf16x2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
           const uint32_t b = pack_bf16x2(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
           const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-          v[h] = r[0];
-          v[2 + h] = r[1];
+          v[j >> 1][h] = r[0];
+          v[j >> 1][2 + h] = r[1];
         }
-        if (inside || (n0 + i * 16 < p.n && k1 + j * 16 < p.k))
-          __builtin_nontemporal_store(v, (u32x4*)(row + j * 16));
       }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t x = v[0][h], y = v[1][h];
+        halves(x, y);
+        v[0][h] = x;
+        v[1][h] = y;
+      }
+      if (inside || (n0 + i * 16 < p.n && k1 < p.k)) __builtin_nontemporal_store(v[0], (u32x4*)row);
+      if (inside || (n0 + i * 16 + 8 < p.n && k1 < p.k)) __builtin_nontemporal_store(v[1], (u32x4*)(row + 8 * p.lddw));
       __builtin_amdgcn_sched_barrier(0);
     }
     return inside;
