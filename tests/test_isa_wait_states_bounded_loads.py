@@ -48,4 +48,4 @@ def test_every_path_to_a_bounded_load_of_the_built_library(tmp_path):
             loads, bad = scan(bounded(body))
             total += loads
             assert not bad, f"{len(bad)} of {loads} loads, e.g. {bad[:3]}"
-    assert total >= 8 * 4 * 4
+    assert total >= 8 * 4 * 2   # eight kernels, a stage of four loads where they begin and in a step
