@@ -356,12 +356,16 @@ hipError_t norm_grad(const NormGradParams& p, hipStream_t stream) {
 
 }  // namespace
 
-// As many as run at once, each with the same number of rows but for the last few.
+// As many as run at once, each with the same number of rows but for the last few.  Beyond 1024 columns, where a workgroup
+// takes row by row, one has up to four rows before there are more than 256: their shares of dw are longer
+// than a row (1000 rows of 2048: 13.1 us and 16.4 with one row each; of 4096 19.9 and 24.2).
 int norm_grad_blocks(int64_t rows, int64_t k) {
   const int64_t at_once = k <= 1024 ? 4 : 1;   // rows that a workgroup takes together
   const int64_t need = (rows + at_once - 1) / at_once;
   const int64_t most = k <= 4096 ? 1024 : 512;
-  const int64_t turns = (need + most - 1) / most;
+  int64_t turns = (need + most - 1) / most;
+  const int64_t some = need / 256 < 4 ? need / 256 : 4;
+  if (at_once == 1 && turns < some) turns = some;
   return (int)(need < 1 ? 1 : (need + turns - 1) / turns);
 }
 

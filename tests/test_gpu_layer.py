@@ -199,7 +199,7 @@ def test_norm_of_rows_with_nan_infinity_and_zeros():
         assert rstd.shape == (0,)
 
 
-@pytest.mark.parametrize("m,k", NORM_SHAPES + [(4099, 264)])
+@pytest.mark.parametrize("m,k", NORM_SHAPES + [(4099, 264), (511, 1032), (1000, 2048), (1030, 4104), (1100, 1048)])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_norm_grad(m, k, dtype):
     h, dy, dh = rows((m, k), dtype, m + k), rows((m, k), dtype, m + k + 1, 0.0), rows((m, k), dtype, m + k + 2, 0.0)
