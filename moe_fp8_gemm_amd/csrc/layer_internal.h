@@ -118,6 +118,7 @@ struct WeightGradParams {
   int accumulate;                 // dw += (fp32 only)
   int splits;                     // workgroups that share a tile's rows
   float* partial;                 // [splits, groups, n, k] where splits > 1
+  int past_l2;                    // the launch's own: how dW is written
 };
 
 hipError_t launch_norm(const NormParams& p, int dtype, int out, hipStream_t stream);

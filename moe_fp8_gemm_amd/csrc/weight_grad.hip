@@ -21,8 +21,8 @@
 //
 // Bound by matrix instructions, at the clock that the card's power leaves them (1.9 to 2.2 GHz), where groups have
 // many rows, and by the operands' and dW's way through memory where they have few.  Measured, with operands that no
-// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 521 us with fp32 sums (923 TFLOP/s, 940 MB of dW) and
-// 459 us in bf16 (1048), 16-bit rows 507 and 436 us; 64 experts, 16384 rows, 2048 x 1408: codes 209 and 156 us
+// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 538 us with fp32 sums (894 TFLOP/s, 940 MB of dW) and
+// 468 us in bf16 (1027), 16-bit rows 510 and 440 us; 64 experts, 16384 rows, 2048 x 1408: codes 210 and 156 us
 // (738 MB of fp32, 369 of bf16), 16-bit rows 221 and 160 us; a dense 8191 x 512 x 2176 in 33 us.
 // Before dW went out in whole lines 576 and 484, 258 and 172 us (codes): half lines reached memory 1.46 times.  Before
 // that, with a prologue for each tile, 600 and 507, 260 and 199 us.
@@ -435,9 +435,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
           __builtin_amdgcn_sched_barrier(0);   // no more than a row's addresses and sums at once
         }
       };
-      // dW passes L2 by, which the operands need; the splits' sums are read again at once
+      // dW passes L2 by, which the operands need, where whole lines can; the splits' sums are read again at once
       if (add) each([&](f32x4* dst, f32x4 v) { *dst = *dst + v; });
-      else if (p.splits > 1) each([&](f32x4* dst, f32x4 v) { *dst = v; });
+      else if (p.splits > 1 || !p.past_l2) each([&](f32x4* dst, f32x4 v) { *dst = v; });
       else each([&](f32x4* dst, f32x4 v) { __builtin_nontemporal_store(v, dst); });
       return inside && !add && kF32;
     }
@@ -446,32 +446,37 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     uint16_t* dw = (uint16_t*)p.dw + w.g * p.dw_gs;
     const int64_t k1 = k0 + upper * 32 + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
     static_assert(C::kFragK == 4, "two stores of two fragments");
+    auto each = [&](auto&& f) {
 #pragma unroll
-    for (int i = 0; i < C::kFragN; ++i) {
-      uint16_t* row = dw + (n0 + i * 16) * p.lddw + k1;
-      u32x4 v[2];
+      for (int i = 0; i < C::kFragN; ++i) {
+        uint16_t* row = dw + (n0 + i * 16) * p.lddw + k1;
+        u32x4 v[2];
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
+        for (int j = 0; j < 4; j += 2) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = pack_bf16x2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-          const uint32_t b = pack_bf16x2(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
-          const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-          v[j >> 1][h] = r[0];
-          v[j >> 1][2 + h] = r[1];
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = pack_bf16x2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+            const uint32_t b = pack_bf16x2(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
+            const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+            v[j >> 1][h] = r[0];
+            v[j >> 1][2 + h] = r[1];
+          }
         }
-      }
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t x = v[0][h], y = v[1][h];
-        halves(x, y);
-        v[0][h] = x;
-        v[1][h] = y;
+        for (int h = 0; h < 4; ++h) {
+          uint32_t x = v[0][h], y = v[1][h];
+          halves(x, y);
+          v[0][h] = x;
+          v[1][h] = y;
+        }
+        if (inside || (n0 + i * 16 < p.n && k1 < p.k)) f((u32x4*)row, v[0]);
+        if (inside || (n0 + i * 16 + 8 < p.n && k1 < p.k)) f((u32x4*)(row + 8 * p.lddw), v[1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (inside || (n0 + i * 16 < p.n && k1 < p.k)) __builtin_nontemporal_store(v[0], (u32x4*)row);
-      if (inside || (n0 + i * 16 + 8 < p.n && k1 < p.k)) __builtin_nontemporal_store(v[1], (u32x4*)(row + 8 * p.lddw));
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    };
+    // two loops: the compiler would make one store of two that only differ in their way
+    if (p.past_l2) each([&](u32x4* dst, u32x4 v) { __builtin_nontemporal_store(v, dst); });
+    else each([&](u32x4* dst, u32x4 v) { *dst = v; });
     return inside;
   };
 
@@ -598,8 +603,18 @@ int weight_grad_splits(int64_t rows, int64_t n, int64_t k, int groups) {
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-hipError_t launch_weight_grad(const WeightGradParams& p, bool x_fp8, int out_dtype, hipStream_t stream) {
+// dW's rows begin at multiples of 64 bytes: what a workgroup writes of them are whole lines, or halves at its edges.
+// Elsewhere the pieces of a line have to meet in L2.  16-bit rows, 64 experts of 10 rows, 1152 x k, past L2 and
+// through it: k 1152 78 and 80 us (fp32), 41 and 44 (bf16), 1160 168 and 96, 87 and 54; of 256 rows on average
+// 1152 110 and 142, 84 and 101, 1160 168 and 143, 94 and 104; 8 of 1024, 4096 x 7176: 639 and 554, 498 and 479.
+static bool whole_lines(const WeightGradParams& p, int64_t elem) {
+  return (uintptr_t)p.dw % 64 == 0 && p.lddw * elem % 64 == 0 && (p.groups == 1 || p.dw_gs * elem % 64 == 0);
+}
+
+hipError_t launch_weight_grad(const WeightGradParams& given, bool x_fp8, int out_dtype, hipStream_t stream) {
   const bool f32 = out_dtype == DG_F32;
+  WeightGradParams p = given;
+  p.past_l2 = whole_lines(p, f32 ? 4 : 2);
   const hipError_t err = launch(p, x_fp8, f32, stream);
   if (err != hipSuccess || p.splits <= 1) return err;
   const int64_t all = (int64_t)p.groups * p.n * (p.k / 4);
