@@ -491,6 +491,8 @@ PyObject* norm(PyObject* const* args, const char* name, const char* abi) {
   same_device(a, x, {&w, &r, &c.q, &c.sf, &y, &h, &rstd});
   TORCH_CHECK_VALUE(!y.defined() || !h.defined() || rows == 0 || k == 0 || y.data_ptr() != h.data_ptr(), a.call,
                     ": y and h must be different tensors");
+  TORCH_CHECK_VALUE(!y.defined() || h.defined() || rows == 0 || k == 0 || y.data_ptr() != x.data_ptr(), a.call,
+                    ": y would overwrite x, which is the h that is returned; give h, or another y");
   void* const rp = r.defined() ? ptr(r) : nullptr;
   void* const wp = w.defined() ? ptr(w) : nullptr;
   void* const hp = h.defined() ? ptr(h) : nullptr;

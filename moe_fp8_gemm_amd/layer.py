@@ -36,7 +36,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
 
     x float32, bfloat16 or float16 [rows, k] (k a multiple of 8 up to 16384); residual like x, or None: h is x itself;
     weight [k] of x's type or float32, or None: ones.  y and h have x's type, rstd float32 [rows].  The norm is that of
-    the rounded h.  y and h may be given x or residual to be written in place.
+    the rounded h.  y and h may be given x or residual to be written in place, y not x where x is the h that is returned
+    (no residual, no h given).
     """
     return _native.rms_norm(x, weight, residual, eps, y, h, rstd)
 
