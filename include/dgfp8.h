@@ -731,7 +731,8 @@ dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t 
  * 1.8e19 overflows its square: rstd is 0 then.  A NaN or an infinity makes its row NaN
  * (where it is finite, 0).
  * Limits: k % 8 == 0, k <= 16384, rows <= 2^23 (2^21 where k > 8192) -> otherwise
- * DG_ERROR_NOT_SUPPORTED, as for misaligned rows.
+ * DG_ERROR_NOT_SUPPORTED, as for misaligned rows.  k == 0: nothing is written, rstd and int8 scales
+ * neither.
  */
 dg_status dg_rms_norm(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, int weight_dtype, float eps, void* h, int64_t ldh,
@@ -794,7 +795,7 @@ dg_status dg_swiglu_cast_fp8(const void* h, int dtype, int64_t ldh, const int32_
                              int64_t rows, int64_t inner, int ue8m0, void* stream);
 
 /* The same with the int8 cast: q int8 [rows, inner], sf fp32 [rows] with stride sf_s.
- * inner % 16 == 0, inner <= 16384. */
+ * inner % 16 == 0, inner <= 16384.  inner == 0: the scales of rows of zeros. */
 dg_status dg_swiglu_cast_int8(const void* h, int dtype, int64_t ldh, const int32_t* m_indices,
                               const int32_t* masked_m, int num_groups, void* q, int64_t ldq,
                               float* sf, int64_t sf_s, int64_t rows, int64_t inner, void* stream);

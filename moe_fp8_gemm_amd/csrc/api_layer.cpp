@@ -220,9 +220,13 @@ DG_EXPORT dg_status dg_swiglu_cast_int8(const void* h, int dtype, int64_t ldh, c
   if (!is_dtype(dtype) || rows < 0 || inner < 0) return DG_ERROR_INVALID_VALUE;
   SwigluParams p{};
   dg_status st = check_set(p.at, m_indices, masked_m, num_groups, rows);
-  if (st != DG_SUCCESS || rows == 0 || inner == 0) return st;
-  if ((st = check_rows(h, ldh, 2 * inner, elem_bytes(dtype))) != DG_SUCCESS) return st;
-  if ((st = check_codes(q, ldq, inner, sf, sf_s, 0)) != DG_SUCCESS) return st;
+  if (st != DG_SUCCESS || rows == 0) return st;
+  if (inner == 0) {   // rows without columns have a scale all the same
+    if ((st = check_scales(sf, sf_s, 0)) != DG_SUCCESS) return st;
+  } else {
+    if ((st = check_rows(h, ldh, 2 * inner, elem_bytes(dtype))) != DG_SUCCESS) return st;
+    if ((st = check_codes(q, ldq, inner, sf, sf_s, 0)) != DG_SUCCESS) return st;
+  }
   if (inner % 16 != 0 || inner > kMaxInnerInt8 || rows > kMaxRows) return DG_ERROR_NOT_SUPPORTED;
   p.h = h; p.ldh = ldh; p.inner = inner;
   p.q = static_cast<uint8_t*>(q); p.ldq = ldq; p.sf = sf; p.sf_s0 = sf_s;

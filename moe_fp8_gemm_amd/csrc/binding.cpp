@@ -9,6 +9,8 @@
 // than DG_SUCCESS the package's DgError.
 #include <Python.h>
 
+#include <cmath>
+
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
@@ -512,6 +514,10 @@ PyObject* norm(PyObject* const* args, const char* name, const char* abi) {
                                ptr(c.q), ld(c.q), ptr<float>(c.sf), c.sf.stride(0), rows, k, on.stream);
   }
   if (!done(st, abi)) return nullptr;
+  if (k == 0 && rows > 0) {   // nothing was launched: the mean of no squares, and the scale of a row without a maximum
+    rstd.fill_(NAN);
+    if (kKind == 2) c.sf.fill_(1e-4f / 127.0f);
+  }
   PyObject* hr = h.defined() ? THPVariable_Wrap(h) : Py_NewRef(args[0]);
   if (kKind == 0) return Py_BuildValue("(NNN)", THPVariable_Wrap(y), hr, THPVariable_Wrap(rstd));
   return Py_BuildValue("(NNN)", pair(c.q, c.sf), hr, THPVariable_Wrap(rstd));

@@ -37,7 +37,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     x float32, bfloat16 or float16 [rows, k] (k a multiple of 8 up to 16384); residual like x, or None: h is x itself;
     weight [k] of x's type or float32, or None: ones.  y and h have x's type, rstd float32 [rows].  The norm is that of
     the rounded h.  y and h may be given x or residual to be written in place, y not x where x is the h that is returned
-    (no residual, no h given).
+    (no residual, no h given).  Without columns rstd is NaN: the mean of nothing.
     """
     return _native.rms_norm(x, weight, residual, eps, y, h, rstd)
 
@@ -61,7 +61,8 @@ def rms_norm_cast_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, r
                        *, eps: float = 1e-6, q: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None,
                        y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
                        rstd: Optional[torch.Tensor] = None) -> Tuple[Pair, torch.Tensor, torch.Tensor]:
-    """As ``rms_norm_cast_fp8`` with the int8 cast: (int8 codes [rows, k], fp32 scales [rows]), k a multiple of 16."""
+    """As ``rms_norm_cast_fp8`` with the int8 cast: (int8 codes [rows, k], fp32 scales [rows]), k a multiple of 16.
+    Without columns the scales are those of rows of zeros."""
     return _native.rms_norm_cast_int8(x, weight, residual, eps, q, sf, y, h, rstd)
 
 
@@ -103,7 +104,7 @@ def swiglu_cast_int8(h: torch.Tensor, *, m_indices: Optional[torch.Tensor] = Non
                      masked_m: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
                      sf: Optional[torch.Tensor] = None) -> Pair:
     """As ``swiglu_cast_fp8`` with the int8 cast: (int8 codes [rows, n], fp32 scales [rows]), n a multiple of 16 up to
-    16384."""
+    16384.  Without columns the scales are those of rows of zeros."""
     return _native.swiglu_cast_int8(h, m_indices, masked_m, q, sf)
 
 

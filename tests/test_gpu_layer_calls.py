@@ -33,3 +33,30 @@ def test_norm_does_not_write_y_over_the_h_that_it_returns(norm):
     x.copy_(kept)
     _, got, _ = norm(x, y=y)
     assert got is x and torch.equal(x, kept)
+
+
+def test_rows_without_columns():
+    """What does not depend on columns is written: NaN for the mean of nothing, and the scale that a row of zeros has."""
+    e = torch.empty((5, 0), dtype=BF16, device=device())
+    zeros = torch.zeros((5, 128), dtype=BF16, device=device())
+    floor = dg.per_token_cast_int8(zeros)[1]
+    for norm in (dg.rms_norm, dg.rms_norm_cast_fp8, dg.rms_norm_cast_int8):
+        for residual in (None, e):
+            rstd = torch.full((5,), 7.0, device=device())
+            out, h, got = norm(e, None, residual, rstd=rstd)
+            assert got is rstd and h.shape == (5, 0) and bool(rstd.isnan().all())
+    sf = torch.full((10,), 7.0, device=device())
+    dg.rms_norm_cast_int8(e, sf=sf[::2])
+    assert torch.equal(sf[::2], floor) and bool((sf[1::2] == 7).all())
+    sf = torch.full((5,), 7.0, device=device())
+    q, got = dg.swiglu_cast_int8(e, sf=sf)
+    assert got is sf and q.shape == (5, 0) and torch.equal(sf, floor)
+    sf.fill_(7)
+    dg.swiglu_cast_int8(e, m_indices=torch.tensor([0, -1, 2, -1, 0], dtype=torch.int32, device=device()), sf=sf)
+    assert torch.equal(sf[::2], floor[::2]) and bool((sf[1::2] == 7).all())
+    sf = torch.full((4,), 7.0, device=device())
+    dg.swiglu_cast_int8(e[:4], masked_m=torch.tensor([1, 5], dtype=torch.int32, device=device()), sf=sf)
+    assert torch.equal(sf[[0, 2, 3]], floor[:3]) and sf[1] == 7
+    dx, dw = dg.rms_norm_grad(e, e, torch.empty(0, device=device()), torch.ones(5, device=device()))
+    assert dx.shape == (5, 0) and dw.shape == (0,)
+    assert dg.swiglu_cast_fp8(e)[1].shape == (5, 0) and dg.swiglu_grad(e, e).shape == (5, 0)
