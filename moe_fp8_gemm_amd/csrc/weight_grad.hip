@@ -186,12 +186,14 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) weight_grad_kernel(WeightGradParams p
     w.n0 = (band * 4 + in - across * high) * C::kTn;
     w.k0 = across * C::kTk;
     const int first = uniform(((DG_LAS int32_t*)group_first)[w.g]);
-    const int count = uniform(((DG_LAS int32_t*)group_count)[w.g]);
-    const int all = (count + kStep - 1) / kStep, share = uniform((all + p.splits - 1) / p.splits);
+    // below 2^31; whole stages of that many rows are 2^31 rows, one more than an int holds
+    const uint32_t count = (uint32_t)uniform(((DG_LAS int32_t*)group_count)[w.g]);
+    const int all = (int)((count + (kStep - 1)) / kStep), share = uniform((all + p.splits - 1) / p.splits);
     const int s0 = w.split * share < all ? w.split * share : all;
     w.stages = share < all - s0 ? share : all - s0;
     w.row = (int64_t)first + (int64_t)s0 * kStep;
-    w.left = count - s0 * kStep < w.stages * kStep ? count - s0 * kStep : w.stages * kStep;
+    const uint32_t rest = count - (uint32_t)s0 * kStep, whole = (uint32_t)w.stages * kStep;
+    w.left = (int)(rest < whole ? rest : whole);
     return w;
   };
 

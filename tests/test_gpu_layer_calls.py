@@ -60,3 +60,25 @@ def test_rows_without_columns():
     dx, dw = dg.rms_norm_grad(e, e, torch.empty(0, device=device()), torch.ones(5, device=device()))
     assert dx.shape == (5, 0) and dw.shape == (0,)
     assert dg.swiglu_cast_fp8(e)[1].shape == (5, 0) and dg.swiglu_grad(e, e).shape == (5, 0)
+
+
+def test_weight_grad_of_as_many_rows_as_there_can_be():
+    """2^31 - 1 rows of one group, 34 GB: zeros but for a few rows of whole numbers, whose products are exact."""
+    rows, n = 2 ** 31 - 1, 8
+    dy = torch.zeros((rows, n), dtype=BF16, device=device())
+    at = torch.tensor([0, 31, 2 ** 20 + 3, 2 ** 30, 2 ** 31 - 34, 2 ** 31 - 33, 2 ** 31 - 2], device=device())
+    dy[at] = ((torch.arange(7 * n, device=device()).view(7, n) * 5) % 13 - 6).to(BF16)
+    few = dy[at].double()
+    want = (few.t() @ few).float()
+    count = torch.tensor([rows], dtype=torch.int32, device=device())
+    assert dg.lib.dg_weight_grad_workspace_size(rows, n, n, 1) > 0
+    dw = torch.empty((n, n), device=device())
+    assert torch.equal(dg.weight_grad(dy, dy, dw), want)
+    for f in (dg.m_grouped_weight_grad_contiguous, dg.m_grouped_weight_grad_masked):
+        dw = torch.ones((1, n, n), device=device())
+        assert torch.equal(f(dy, dy, dw, count, accumulate=True)[0], want + 1)
+    count -= 31                                   # the last rows are behind the last whole stage
+    dy[-31:] = float("nan")
+    few[-1] = 0
+    dw = torch.empty((1, n, n), device=device())
+    assert torch.equal(dg.m_grouped_weight_grad_contiguous(dy, dy, dw, count)[0], (few.t() @ few).float())
