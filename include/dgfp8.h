@@ -834,8 +834,9 @@ dg_status dg_swiglu_grad(const void* da, int dtype, int64_t ldda, const void* h,
  *             matter): lets several workgroups share a tile's rows where there are few tiles; NULL
  *             or smaller: they do not.  Calls that may overlap need distinct ones
  * Sums are fp32, in an order that the sizes, num_groups and whether ws is there alone give.
- * Limits: n % 8 == 0, k % 8 == 0 (codes: k % 128 == 0), n, k, lddy, ldx, sf_sm < 2^24, rows < 2^31, rows of
- * dy, x and dw at 16-byte boundaries -> otherwise DG_ERROR_NOT_SUPPORTED.  rows == 0 gives zeros.
+ * Limits: n % 8 == 0, k % 8 == 0 (codes: k % 128 == 0), n, k, lddy, ldx, sf_sm < 2^24, rows < 2^31, at
+ * most 2^22 tiles of 128 x 128 in dw (of all groups), rows of dy, x and dw at 16-byte boundaries ->
+ * otherwise DG_ERROR_NOT_SUPPORTED.  rows == 0 gives zeros.
  */
 dg_status dg_weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                          const float* sf, int64_t sf_sm, int64_t sf_sk,

@@ -105,7 +105,7 @@ dg_status weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   if (n % 8 != 0 || k % (sf ? 128 : 8) != 0 || n > kMaxLd || k > kMaxLd) return DG_ERROR_NOT_SUPPORTED;
   if (rows >= (int64_t)1 << 31 || groups > kMaxGroups || !aligned(counts, 4)) return DG_ERROR_NOT_SUPPORTED;
   if (!aligned(ws, 16)) return DG_ERROR_NOT_SUPPORTED;
-  // a workgroup of at most 512 threads for each 128 x 128 tile
+  // the kernel counts tiles, and a round of workgroups past the last, in int: 2^22 tiles, 256 GB of fp32, leave room
   if (ceil_div(n, 128) * ceil_div(k, 128) * groups > (int64_t)1 << 22) return DG_ERROR_NOT_SUPPORTED;
   int splits = weight_grad_splits(rows, n, k, groups);
   if (!ws || ws_bytes < (size_t)splits * groups * n * k * sizeof(float)) splits = 1;
