@@ -96,6 +96,7 @@ dg_status weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   if (st != DG_SUCCESS) return st;
   if (groups > 1 && dw_group_stride < 0) return DG_ERROR_INVALID_VALUE;
   if (!strides_ok({dw_group_stride}) || (groups > 1 && dw_group_stride * el % 16 != 0)) return DG_ERROR_NOT_SUPPORTED;
+  if (groups > 1 && dw_group_stride < k) return DG_ERROR_INVALID_VALUE;   // they would write each other's elements
   if (rows > 0) {
     if ((st = check_rows(dy, lddy, n, 2)) != DG_SUCCESS) return st;
     if ((st = check_rows(x, ldx, k, sf ? 1 : 2)) != DG_SUCCESS) return st;

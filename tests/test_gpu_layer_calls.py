@@ -82,3 +82,24 @@ def test_weight_grad_of_as_many_rows_as_there_can_be():
     few[-1] = 0
     dw = torch.empty((1, n, n), device=device())
     assert torch.equal(dg.m_grouped_weight_grad_contiguous(dy, dy, dw, count)[0], (few.t() @ few).float())
+
+
+def test_weight_grad_refuses_groups_in_one_place_and_takes_interleaved_ones():
+    """An expanded dw would be written by all groups at once; rows of the groups in turn are as good as any other."""
+    dy, x = (torch.randn((64, w), device=device()).to(BF16) for w in (24, 128))
+    counts = torch.tensor([30, 0, 34], dtype=torch.int32, device=device())
+    masked = torch.tensor([32, 30], dtype=torch.int32, device=device())
+    for f, c in ((dg.m_grouped_weight_grad_contiguous, counts), (dg.m_grouped_weight_grad_masked, masked)):
+        g = c.shape[0]
+        kept = torch.full((1, 24, 128), 7.0, device=device())
+        with pytest.raises(dg.DgError):
+            f(dy, x, kept.expand(g, -1, -1), c)
+        assert bool((kept == 7).all())
+        one = dict(alignment=1) if c is counts else {}
+        want = f(dy, x, torch.empty((g, 24, 128), device=device()), c, **one)
+        turns = torch.empty((24, g, 128), device=device()).transpose(0, 1)
+        assert f(dy, x, turns, c, **one) is turns and torch.equal(turns, want)
+    one = torch.tensor([64], dtype=torch.int32, device=device())
+    dw = torch.empty((24, 128), device=device())
+    got = dg.m_grouped_weight_grad_contiguous(dy, x, dw.expand(1, -1, -1), one)        # one group: no other's place
+    assert torch.equal(got[0], dg.weight_grad(dy, x, torch.empty_like(dw)))

@@ -27,3 +27,10 @@ def test_weight_grad_of_too_many_tiles(n, k, groups):
     kw = dict(wide(n, k), groups=groups, dw_gs=n * k)
     assert call(lib.dg_m_grouped_weight_grad_contiguous, WGRAD_CONTIGUOUS, **kw) == UNSUPPORTED
     assert call(lib.dg_m_grouped_weight_grad_masked, WGRAD_MASKED, **kw) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,status", [(dict(dw_gs=0), INVALID), (dict(dw_gs=252), INVALID), (dict(dw_gs=-256), INVALID),
+                                       (dict(dw_gs=0, out=1, accumulate=0), INVALID), (dict(dw_gs=2), UNSUPPORTED)])
+def test_weight_grad_of_groups_in_one_place(kw, status):
+    assert call(lib.dg_m_grouped_weight_grad_contiguous, WGRAD_CONTIGUOUS, **kw) == status
+    assert call(lib.dg_m_grouped_weight_grad_masked, WGRAD_MASKED, **kw) == status
