@@ -566,9 +566,12 @@ __global__ void __launch_bounds__(256) weight_grad_sum_kernel(WeightGradParams p
 
 int64_t tiles(int64_t n, int64_t k, int64_t tn, int64_t tk) { return ((n + tn - 1) / tn) * ((k + tk - 1) / tk); }
 
-// 128 x 128 tiles, two workgroups a CU, as long as all of them run at once; 256 x 256 tiles, which read less for each
-// product, beyond.  8192 rows, bf16, fp32 sums: 2048 x 4096 (128 big tiles) 137 us in small tiles and 179 in big
-// ones, 4096 x 2816 (176) 254 and 183, 4096 x 4096 269 and 223.
+// 256 x 256 tiles, which read less for each product, from 129 of them on; 128 x 128 tiles, two workgroups a CU, below:
+// where n and k are multiples of 256 as many small tiles as run at once.  8192 rows, bf16, fp32 sums: 2048 x 4096 (128
+// big tiles) 137 us in small tiles and 179 in big ones, 4096 x 2816 (176) 254 and 183, 4096 x 4096 269 and 223.
+// Where n or k are not, small tiles could run at once beyond that (up to 512 of them), and win or lose: 8192 rows, 2064 x
+// 3840 (135 big, 510 small) 150 and 178 us; 170 groups of 256 rows, 128 x 384 19 and 29; 256 groups, 128 x 128, of 128
+// rows 15.6 and 18.8, of 1024 rows 51.8 and 45.5; 512 groups of 64 rows, 64 x 128 37.6 and 30.5.
 bool big_tiles(int64_t n, int64_t k, int groups) { return tiles(n, k, 256, 256) * groups > 128; }
 
 template <class C>
