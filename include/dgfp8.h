@@ -720,6 +720,8 @@ dg_status dg_combine_grad(const void* dout, int64_t ldo, const void* y, int64_t 
  *   h = x + residual, rounded to x's type;
  *   rstd = (sum h^2 / k + eps)^-1/2;   y = h * rstd * weight, rounded to x's type.
  * The norm is that of the rounded h, so that h and rstd are all its gradient needs.
+ * y's fp32 value is (h * weight) * rstd: a product of 16-bit h and weight is exact, so that one
+ * rounding stands before the store or the cast (h * weight past fp32's range shows).
  *   x         device, dtype [rows, k], row stride ldx
  *   residual  device, dtype [rows, k], row stride ldr, or NULL: h = x
  *   weight    device, [k] of weight_dtype (dtype or DG_F32), 16-byte aligned, or NULL: ones
