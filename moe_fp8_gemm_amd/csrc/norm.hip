@@ -14,7 +14,7 @@
 // written once, past L2 where nothing near reads it.  Measured, bf16: 32768 rows of 7168 with residual to FP8
 // (1.65 GB) 283 us, 5.8 TB/s; one such row 3.9 us, of which a launch that does nothing has 3.6; gradient of 16384
 // rows with dh (0.94 GB) 181 us, 5.2 TB/s; 4099 rows of 2048 24 us, of which the sum of the workgroups' shares of dw
-// is about 6.  Rows in a run for each XCD's L2 296 us, stores through the caches 290.
+// is about 5.  Rows in a run for each XCD's L2 296 us, stores through the caches 290.
 #include "cast_rules.h"
 #include "elem_types.h"
 #include "layer_internal.h"

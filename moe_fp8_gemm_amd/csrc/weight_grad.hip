@@ -3,8 +3,9 @@
 //
 // Mathematics.  A product whose contraction runs over rows, the slow dimension of both operands.  dy and x
 // enter the bf16 matrix instructions; a code times its scale is rounded to bf16 (not at all where the
-// scale is a power of two, as with exponent-only scales: 4 significant bits stay).  Sums are
-// fp32.
+// scale is a power of two, as with exponent-only scales: 4 significant bits stay).  That is 2^-9 of a term at most,
+// where the code stands for its value within 2^-4; in two halves of 8 bits the product would be all but exact and
+// take twice the matrix instructions.  The caller who wants it exact casts with exponent-only scales.  Sums are fp32.
 //
 // Rows.  A stage is 32 rows of both operands as they lie in memory, brought to LDS by direct loads
 // through buffer descriptors that end with the segment's last row: what lies behind reads as
@@ -21,9 +22,10 @@
 //
 // Bound by matrix instructions, at the clock that the card's power leaves them (1.9 to 2.2 GHz), where groups have
 // many rows, and by the operands' and dW's way through memory where they have few.  Measured, with operands that no
-// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 538 us with fp32 sums (894 TFLOP/s, 940 MB of dW) and
-// 468 us in bf16 (1027), 16-bit rows 510 and 440 us; 64 experts, 16384 rows, 2048 x 1408: codes 210 and 156 us
-// (738 MB of fp32, 369 of bf16), 16-bit rows 221 and 160 us; a dense 8191 x 512 x 2176 in 33 us.
+// cache holds: 8 experts, 8192 rows, 4096 x 7168: codes 541 us with fp32 sums (889 TFLOP/s, 940 MB of dW) and
+// 468 us in bf16 (1027), 16-bit rows 510 and 440 us; 64 experts, 16384 rows, 2048 x 1408: codes 210 and 159 us
+// (738 MB of fp32, 369 of bf16), 16-bit rows 221 and 160 us; a dense 8191 x 512 x 2176 in 33 us.  Added to dW, which
+// is read after a tile's last product: 8 experts of 1024 rows 763 us (527 without), 64 of 256 437 (196).
 // Before dW went out in whole lines 576 and 484, 258 and 172 us (codes): half lines reached memory 1.46 times.  Before
 // that, with a prologue for each tile, 600 and 507, 260 and 199 us.
 //

@@ -14,6 +14,9 @@ the gradients read what the forward pass kept.  A mixture-of-experts layer's tra
     dh, g = swiglu_grad_cast_fp8(dact, kept, m_indices=layout.m_indices)
     m_grouped_weight_grad_contiguous(dh, a, d_up, layout.counts)
 
+With ``ue8m0=True`` in the casts whose codes a weight's gradient reads, its products are exact; with the casts' default
+scales each value is rounded to bfloat16 first.
+
 Argument marshalling only (in ``csrc/binding.cpp``); the contract is in ``include/dgfp8.h``.  Autograd records none of
 the calls.
 """

@@ -1,4 +1,4 @@
-"""The sigmoid of the gated activation: its error does not grow with the gate.
+"""The sigmoid of the gated activation: its error does not grow with the gate as that of a rounded product's power would.
 
 With u = 2^-24, g in [-87, 87] (e^-g and its reciprocal are normal numbers there), w = 1 - s, s = 1 / (1 + e^-g):
 * t = fl(-g log2 e).  2^t is the hardware's, within a unit of the last place: 2 u.  What t's rounding left out comes back
