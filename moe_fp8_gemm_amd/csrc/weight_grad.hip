@@ -3,7 +3,7 @@
 //
 // Mathematics.  A product whose contraction runs over rows, the slow dimension of both operands.  dy and x
 // enter the bf16 matrix instructions; a code times its scale is rounded to bf16 (not at all where the
-// scale is a power of two, as with exponent-only scales: 4 significant bits stay).  That is 2^-9 of a term at most,
+// scale is a power of two, as with exponent-only scales: 4 significant bits stay).  That is 2^-8 of a term at most,
 // where the code stands for its value within 2^-4; in two halves of 8 bits the product would be all but exact and
 // take twice the matrix instructions.  The caller who wants it exact casts with exponent-only scales.  Sums are fp32.
 //
