@@ -850,7 +850,8 @@ size_t dg_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int num
  * The same for each group (expert) of rows: dw [num_groups, n, k] with group stride
  * dw_group_stride, at least k: no element of dw may belong to two groups.  Groups follow one
  * another, each from a multiple of `alignment` rows (128: dg_expert_layout_contiguous; 1: no
- * padding), counts[g] rows of which count; what lies between them may hold anything.  A group without rows gets zeros (accumulate: nothing).
+ * padding), counts[g] rows of which count; what lies between them may hold anything.  A group
+ * without rows gets zeros (accumulate: nothing).
  *   counts    device, int32 [num_groups]; negative ones count as 0, and rows past `rows` are
  *             left out
  * num_groups <= 1024.
